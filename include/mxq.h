@@ -246,6 +246,159 @@ int mx_grouped_gemm(const uint8_t* qa, const uint8_t* sfa, const uint8_t* qb, co
                     const int32_t* offs, int32_t G, int64_t M, int64_t N, int64_t K, void* out_bf16, void* stream);
 
 /*
+ * ---- operators of the mixture-of-experts layer around the calls above -----------------
+ *
+ * A layer runs: rmsnorm_mx_quantize (the norm before it; codes for the exchange and the
+ * MXFP8 products, bf16 for the router) -> router logits -> moe_route -> moe_plan -> the
+ * tokens gathered by `src` -> mx_grouped_gemm or mxfp4_grouped_gemm over `offs`.
+ */
+
+/* Types of tensors that come in more than one. */
+enum { MXQ_TYPE_BF16 = 0, MXQ_TYPE_F32 = 1 };
+
+/* Score functions of moe_route. */
+enum { MXQ_SCORE_SOFTMAX = 0, MXQ_SCORE_SIGMOID = 1 };
+
+/*
+ * moe_route -- the k experts of each token and their weights.
+ *  logits  (T, E) of `type` (MXQ_TYPE_*), 16-byte aligned; 1 <= E <= 1024.
+ *  bias    (E) fp32 added to the scores for the choice alone (a balancing bias), or NULL.
+ *  Scores p = softmax(logits) over the row, or sigmoid(logits).  Candidates c = p + bias;
+ *  without a bias the logits themselves are compared (both functions are monotone).
+ *  n_groups > 1 (at most 32, dividing E): expert e belongs to group e / (E / n_groups);
+ *  only candidates of the top_groups groups with the largest sums of their group_top (1 or
+ *  2; fewer where a group has fewer) largest c are eligible -- of p, if there is no bias
+ *  and group_top is 2.
+ *  Chosen: the k (1 <= k <= min(E, 32)) largest eligible candidates, in decreasing order;
+ *  equal ones in order of their index (of candidates and of groups).  The choice is that
+ *  of these formulas in 64 bits.
+ *  ids      (T, k) int32; -1 where a row has fewer than k eligible experts.
+ *  weights  (T, k) fp32, 0 where ids is -1.
+ *             w_j = scale * p_j
+ *           or, with renorm, softmax:  w_j = scale * softmax over the chosen logits
+ *                            sigmoid:  w_j = scale * p_j / (sum of the chosen p + 1e-20).
+ *  A logit of -inf, or a bias of -inf, masks its expert: it is never chosen.  A row that
+ *  holds a NaN (or, for softmax, +inf), or whose unmasked experts meet a NaN bias, gets
+ *  ids 0 .. k-1 and NaN weights, so that the fault shows.
+ *  Returns MXQ_OK, MXQ_ERR_ARG (an enum, n_groups, top_groups, group_top, a scale that is
+ *  not finite), MXQ_ERR_SHAPE, MXQ_ERR_NULL, MXQ_ERR_ALIGN or MXQ_ERR_CUDA.
+ */
+int moe_route(const void* logits, int type, int64_t T, int64_t E, const float* bias, int score, int32_t n_groups,
+              int32_t top_groups, int32_t group_top, int32_t k, int renorm, float scale, float* weights,
+              int32_t* ids, void* stream);
+
+/*
+ * moe_route_backward -- the gradient of the logits.
+ *  ids (T, k) as moe_route wrote them (entries outside 0 .. E-1 are skipped; an index that
+ *  comes twice in a row counts twice), grad_weights (T, k) fp32; logits, score, renorm and
+ *  scale as for moe_route.
+ *  grad_logits (T, E) of the logits' type, 16-byte aligned, must not overlap them: written
+ *  whole.  The choice itself has no gradient; the bias takes none.  Masked experts get 0;
+ *  softmax's gradient reaches every expert of the row, unless renorm confines it to the
+ *  chosen ones.
+ *  Returns as moe_route.
+ */
+int moe_route_backward(const void* logits, int type, int64_t T, int64_t E, const int32_t* ids, int32_t k,
+                       const float* grad_weights, int score, int renorm, float scale, void* grad_logits,
+                       void* stream);
+
+/*
+ * moe_plan -- the rows of the routed slots: a stable sort of the slots by expert.
+ *  ids   n int32 (token t's slots at t k .. t k + k - 1); a value outside 0 .. E-1 routes
+ *        its slot nowhere.  0 <= n < 2^31, 1 <= E <= 1024.
+ *  offs  (E) int32 end offsets, as every per-group call here takes them: expert e's rows
+ *        are [offs[e-1], offs[e]).
+ *  rows  (n) the row of each slot, -1 where it has none.
+ *  src   (n) the slot of each row, in the order of the slots within an expert; -1 for the
+ *        rows at and past offs[E-1].
+ *  workspace  moe_plan_workspace_bytes(n, E) bytes of device memory, 4-byte aligned (NULL
+ *        where that is 0); calls that may run at the same time, and graphs captured from
+ *        them, each need their own.
+ *  Returns MXQ_OK, MXQ_ERR_SHAPE, MXQ_ERR_NULL, MXQ_ERR_ALIGN or MXQ_ERR_CUDA.
+ */
+int moe_plan(const int32_t* ids, int64_t n, int64_t E, int32_t* offs, int32_t* rows, int32_t* src, void* workspace,
+             void* stream);
+
+/* Workspace of moe_plan in bytes; -1 for invalid sizes. */
+int64_t moe_plan_workspace_bytes(int64_t n, int64_t E);
+
+/*
+ * rmsnorm_mx_quantize -- residual addition, root-mean-square norm and MXFP8 quantization.
+ *  x (M, D) bf16; residual (M, D) bf16 or NULL; weight (D) of weight_type; D a multiple of
+ *  32, at most 16384; eps > 0.
+ *    h = bf16_RNE(x + residual), or x;   r = 1 / sqrt(mean_d h^2 + eps)  (fp32);
+ *    y = bf16_RNE(h r weight);           q, s = the row blocks mx_quantize gives for y.
+ *  q (M, D) E4M3, s (M, D/32) E8M0.
+ *  res_out (M, D) bf16 receives h (NULL: not written); it may be x or residual itself.
+ *  y (M, D) bf16 and rstd (M) fp32 (r, for the backward pass) may be NULL.
+ *  All (.., D) tensors 16-byte aligned.  Apart from res_out nothing may overlap.
+ *  Returns MXQ_OK, MXQ_ERR_ARG (a type, eps), MXQ_ERR_SHAPE, MXQ_ERR_NULL, MXQ_ERR_ALIGN
+ *  or MXQ_ERR_CUDA.
+ */
+int rmsnorm_mx_quantize(const void* x_bf16, const void* residual_bf16, const void* weight, int weight_type,
+                        int64_t M, int64_t D, float eps, void* res_out_bf16, void* y_bf16, uint8_t* q, uint8_t* s,
+                        float* rstd, void* stream);
+
+/*
+ * rmsnorm_backward -- gradients of the norm (the quantization passes its gradient straight
+ * through).  With n = h rstd and g = grad_y weight:
+ *    grad_x = bf16_RNE( rstd (g - n mean_d(g n)) + grad_res ),   grad_weight = sum_m grad_y n.
+ *  grad_y, h (the forward pass's res_out, or its x) (M, D) bf16; rstd (M) fp32; grad_res
+ *  (M, D) bf16, the gradient that reaches res_out, or NULL.
+ *  grad_x (M, D) bf16: the gradient of x and of residual alike; it may be grad_y or
+ *  grad_res itself.  grad_weight (D) fp32, written whatever M is (zeros for M = 0).
+ *  workspace  rmsnorm_backward_workspace_bytes(M, D) bytes, 16-byte aligned, one for each
+ *  call that may run at the same time.  The sums' order is fixed for given sizes.
+ *  Returns as rmsnorm_mx_quantize.
+ */
+int rmsnorm_backward(const void* grad_y_bf16, const void* h_bf16, const void* weight, int weight_type,
+                     const float* rstd, const void* grad_res_bf16, int64_t M, int64_t D, void* grad_x_bf16,
+                     float* grad_weight, void* workspace, void* stream);
+
+/* Workspace of rmsnorm_backward in bytes; -1 for invalid sizes. */
+int64_t rmsnorm_backward_workspace_bytes(int64_t M, int64_t D);
+
+/*
+ * mxfp4_quantize -- MXFP4 quantize of a bf16 tensor along its rows: blocks of 32 E2M1 codes
+ * (1 sign, 2 exponent, 1 mantissa bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6) under one E8M0 scale,
+ *    b = clamp(floor(log2(amax)) - 2, -127, 127) + 127 (all-zero block: 0),
+ *    code = satRNE_E2M1(x * 2^(127-b));
+ *  a block holding Inf or NaN gets b = 0xFF and codes 7 | sign.
+ *  x (batch, rows, cols) bf16, cols a multiple of 32; q (batch, rows, cols/2), the even
+ *  element of each pair in the low four bits.  Both 16-byte aligned.
+ *  s           (batch, rows, cols/32) E8M0, or NULL;
+ *  sf_blocked  the same scales as mx_scales_to_blocked would rearrange them with these offs
+ *              and G (mx_scales_blocked_bytes(batch, rows, cols/32, G) bytes, 16-byte
+ *              aligned), or NULL.  At least one of the two.
+ *  offs, G     G > 0 (batch must be 1, sf_blocked given): the int32 end offsets of the
+ *              rows' groups, device memory; rows in no group are neither read nor written.
+ *  Returns MXQ_OK, MXQ_ERR_SHAPE, MXQ_ERR_NULL, MXQ_ERR_ALIGN or MXQ_ERR_CUDA.
+ */
+int mxfp4_quantize(const void* x_bf16, int64_t batch, int64_t rows, int64_t cols, uint8_t* q, uint8_t* s,
+                   uint8_t* sf_blocked, const int32_t* offs, int32_t G, void* stream);
+
+/*
+ * mxfp4_dequantize -- back to bf16: y = bf16_RNE(E2M1(code) * 2^(b-127)), NaN (0x7FC0)
+ * under a scale of 0xFF.  q (rows, cols/2), s (rows, cols/32) plain, y (rows, cols) bf16;
+ * q and y 16-byte aligned, cols a multiple of 32 (a batch: rows = all its rows).
+ */
+int mxfp4_dequantize(const uint8_t* q, const uint8_t* s, int64_t rows, int64_t cols, void* y_bf16, void* stream);
+
+/*
+ * mxfp4_grouped_gemm -- MXFP4 grouped GEMM on the tensor cores (kind::mxf4, two E8M0 scales
+ * per 64 elements of K): as mx_grouped_gemm, with
+ *  qa   (M, K/2) E2M1 code pairs of the tokens, sfa their scales in tiles per group
+ *       (mxfp4_quantize with offs);
+ *  qb   (G, N, K/2), sfb its scales in tiles per matrix (mxfp4_quantize, G = 0);
+ *  out  (M, N) bf16, rounded once from an fp32 accumulator; rows in no group untouched.
+ *  K must be a multiple of 128 and N of 256; all pointers 16-byte aligned (offs 4).
+ *  No scratch memory; waits are bounded and give up as in mx_grouped_gemm.
+ * Returns MXQ_OK, MXQ_ERR_SHAPE, MXQ_ERR_NULL, MXQ_ERR_ALIGN or MXQ_ERR_CUDA.
+ */
+int mxfp4_grouped_gemm(const uint8_t* qa, const uint8_t* sfa, const uint8_t* qb, const uint8_t* sfb,
+                       const int32_t* offs, int32_t G, int64_t M, int64_t N, int64_t K, void* out_bf16, void* stream);
+
+/*
  * mx_e4m3_encode_f32 -- the fp32 -> E4M3 conversion every kernel above uses
  * (round to nearest even, magnitudes above 448 saturate to 448, NaN -> 0x7F|sign),
  * exposed so it can be checked exhaustively.  x: n fp32 values, 16-byte aligned;

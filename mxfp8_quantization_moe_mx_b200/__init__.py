@@ -14,6 +14,11 @@ Operations (see include/mxq.h for the exact arithmetic and layouts):
     all in expert parallel", Summary).
   fp8_per_group_rowwise_quant -- per-group rowwise FP8 scaling (torchao "[moe
     training] fix uncoalesced global accesses in per group rowwise scaling kernel").
+  moe_route / moe_route_backward / moe_plan -- the experts of each token, the gradient of
+    the router's logits, and the rows of the grouped products.
+  rmsnorm_mx_quantize / rmsnorm_backward -- residual addition, RMS norm and MXFP8 output.
+  mxfp4_quantize / mxfp4_dequantize / mxfp4_grouped_gemm -- 4-bit codes and their product.
+``mxfp8_quantization_moe_mx_b200.moe`` has the differentiable forms.
 """
 from __future__ import annotations
 
@@ -24,6 +29,7 @@ import torch
 
 ROW, COL = 1, 2
 ROW_MAJOR, COL_MAJOR = 0, 1
+SOFTMAX, SIGMOID = 0, 1
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmxq.so")
@@ -57,6 +63,20 @@ def lib() -> ctypes.CDLL:
         L.fp8_per_group_rowwise_quant_batched.restype = ci
         L.mx_grouped_gemm.argtypes = [vp, vp, vp, vp, vp, i32, i64, i64, i64, vp, vp]
         L.mx_grouped_gemm.restype = ci
+        cf = ctypes.c_float
+        L.moe_route.argtypes = [vp, ci, i64, i64, vp, ci, i32, i32, i32, i32, ci, cf, vp, vp, vp]
+        L.moe_route_backward.argtypes = [vp, ci, i64, i64, vp, i32, vp, ci, ci, cf, vp, vp]
+        L.moe_plan.argtypes = [vp, i64, i64, vp, vp, vp, vp, vp]
+        L.rmsnorm_mx_quantize.argtypes = [vp, vp, vp, ci, i64, i64, cf, vp, vp, vp, vp, vp, vp]
+        L.rmsnorm_backward.argtypes = [vp, vp, vp, ci, vp, vp, i64, i64, vp, vp, vp, vp]
+        L.mxfp4_quantize.argtypes = [vp, i64, i64, i64, vp, vp, vp, vp, i32, vp]
+        L.mxfp4_dequantize.argtypes = [vp, vp, i64, i64, vp, vp]
+        L.mxfp4_grouped_gemm.argtypes = [vp, vp, vp, vp, vp, i32, i64, i64, i64, vp, vp]
+        for f in (L.moe_route, L.moe_route_backward, L.moe_plan, L.rmsnorm_mx_quantize, L.rmsnorm_backward,
+                  L.mxfp4_quantize, L.mxfp4_dequantize, L.mxfp4_grouped_gemm):
+            f.restype = ci
+        L.moe_plan_workspace_bytes.argtypes = L.rmsnorm_backward_workspace_bytes.argtypes = [i64, i64]
+        L.moe_plan_workspace_bytes.restype = L.rmsnorm_backward_workspace_bytes.restype = i64
         for f in (L.mx_quantize, L.mx_dequantize, L.fp8_per_group_rowwise_quant,
                   L.mx_e4m3_encode_f32):
             f.restype = ci
@@ -290,3 +310,214 @@ def mx_grouped_gemm(qa: torch.Tensor, sfa_blocked: torch.Tensor, qb: torch.Tenso
     po = _dev(offs, torch.int32, "offs")
     pout = _dev(out, torch.bfloat16, "out", M * N)
     _check(lib().mx_grouped_gemm(pa, psa, pb, psb, po, G, M, N, K, pout, _stream(stream)))
+
+
+# ---- the operators of a mixture-of-experts layer --------------------------------------------------
+
+class _Args:
+    """The pointers of one call's tensors, which have to lie on one CUDA device."""
+
+    __slots__ = ("device",)
+
+    def __init__(self):
+        self.device = None
+
+    def __call__(self, t: torch.Tensor, dtype, name: str, numel: int | None = None) -> int:
+        p = _dev(t, dtype, name, numel)
+        if self.device is None:
+            self.device = t.device
+        elif t.device != self.device:
+            raise MxqError(f"{name} is on {t.device}, the other tensors are on {self.device}")
+        return p
+
+    def optional(self, t, dtype, name: str, numel: int | None = None):
+        return None if t is None else self(t, dtype, name, numel)
+
+    def typed(self, t: torch.Tensor, name: str, numel: int | None = None) -> tuple[int, int]:
+        """(pointer, type code) of a bf16 or fp32 tensor."""
+        if isinstance(t, torch.Tensor) and t.dtype == torch.float32:
+            return self(t, torch.float32, name, numel), 1
+        return self(t, torch.bfloat16, name, numel), 0
+
+    def run(self, f, *args, stream=None) -> None:
+        """f(*args, stream) on the tensors' device: on its current stream unless one is given."""
+        if self.device.index == torch.cuda.current_device():
+            _check(f(*args, _stream(stream)))
+        else:
+            with torch.cuda.device(self.device):
+                _check(f(*args, _stream(stream)))
+
+
+def _two(t: torch.Tensor, name: str, what: str) -> tuple[int, int]:
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise MxqError(f"{name} must be {what}")
+    return t.shape[0], t.shape[1]
+
+
+def moe_route(logits: torch.Tensor, weights: torch.Tensor, ids: torch.Tensor, bias: torch.Tensor | None = None,
+              score: int = SOFTMAX, n_groups: int = 1, top_groups: int = 1, group_top: int = 1,
+              renorm: bool = False, scale: float = 1.0, stream=None) -> None:
+    """logits bf16 or fp32 (T, E); bias fp32 (E,) or None; weights fp32 (T, k) and ids int32
+    (T, k) receive the k experts of each token and their weights."""
+    T, E = _two(logits, "logits", "(T, E)")
+    k = _two(ids, "ids", "(T, k)")[1]
+    a = _Args()
+    pl, ty = a.typed(logits, "logits")
+    pb = a.optional(bias, torch.float32, "bias", E)
+    pw = a(weights, torch.float32, "weights", T * k)
+    pi = a(ids, torch.int32, "ids", T * k)
+    a.run(lib().moe_route, pl, ty, T, E, pb, score, n_groups, top_groups, group_top, k, bool(renorm), scale, pw, pi,
+          stream=stream)
+
+
+def moe_route_backward(logits: torch.Tensor, ids: torch.Tensor, grad_weights: torch.Tensor,
+                       grad_logits: torch.Tensor, score: int = SOFTMAX, renorm: bool = False, scale: float = 1.0,
+                       stream=None) -> None:
+    """The gradient of moe_route's logits: logits and ids as there, grad_weights fp32
+    (T, k), grad_logits (T, E) of the logits' type (written whole)."""
+    T, E = _two(logits, "logits", "(T, E)")
+    k = _two(ids, "ids", "(T, k)")[1]
+    a = _Args()
+    pl, ty = a.typed(logits, "logits")
+    pi = a(ids, torch.int32, "ids", T * k)
+    pg = a(grad_weights, torch.float32, "grad_weights", T * k)
+    po = a(grad_logits, logits.dtype, "grad_logits", T * E)
+    a.run(lib().moe_route_backward, pl, ty, T, E, pi, k, pg, score, bool(renorm), scale, po, stream=stream)
+
+
+def moe_plan_workspace_bytes(n: int, E: int) -> int:
+    b = int(lib().moe_plan_workspace_bytes(n, E))
+    if b < 0:
+        raise MxqError("invalid sizes for moe_plan")
+    return b
+
+
+def moe_plan(ids: torch.Tensor, offs: torch.Tensor, rows: torch.Tensor, src: torch.Tensor,
+             workspace: torch.Tensor | None = None, stream=None) -> None:
+    """ids int32 (any shape, n slots); offs int32 (E,) receives the experts' end offsets,
+    rows int32 (n) the row of each slot, src int32 (n) the slot of each row; workspace
+    uint8 of moe_plan_workspace_bytes(n, E) (None where that is 0)."""
+    a = _Args()
+    pi = a(ids, torch.int32, "ids")
+    n = ids.numel()
+    po = a(offs, torch.int32, "offs")
+    pr = a(rows, torch.int32, "rows", n)
+    ps = a(src, torch.int32, "src", n)
+    pw = a.optional(workspace, torch.uint8, "workspace")
+    E = offs.numel()
+    if (0 if workspace is None else workspace.numel()) < moe_plan_workspace_bytes(n, E):
+        raise MxqError("workspace is smaller than moe_plan_workspace_bytes")
+    a.run(lib().moe_plan, pi, n, E, po, pr, ps, pw, stream=stream)
+
+
+def rmsnorm_mx_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float, q: torch.Tensor, s: torch.Tensor,
+                        residual: torch.Tensor | None = None, res_out: torch.Tensor | None = None,
+                        y: torch.Tensor | None = None, rstd: torch.Tensor | None = None, stream=None) -> None:
+    """x, residual bf16 (M, D); weight bf16 or fp32 (D,); q uint8 (M, D) and s uint8
+    (M, D/32) receive the MXFP8 norm of x + residual; optional outputs: res_out bf16 (M, D)
+    the sum (may be x or residual itself), y bf16 (M, D) the norm, rstd fp32 (M,)."""
+    M, D = _two(x, "x", "(M, D)")
+    n = M * D
+    a = _Args()
+    bf = torch.bfloat16
+    px = a(x, bf, "x")
+    pw, ty = a.typed(weight, "weight", D)
+    pq = a(q, torch.uint8, "q", n)
+    ps = a(s, torch.uint8, "s", n // 32)
+    pr = a.optional(residual, bf, "residual", n)
+    po = a.optional(res_out, bf, "res_out", n)
+    py = a.optional(y, bf, "y", n)
+    pt = a.optional(rstd, torch.float32, "rstd", M)
+    a.run(lib().rmsnorm_mx_quantize, px, pr, pw, ty, M, D, eps, po, py, pq, ps, pt, stream=stream)
+
+
+def rmsnorm_backward_workspace_bytes(M: int, D: int) -> int:
+    b = int(lib().rmsnorm_backward_workspace_bytes(M, D))
+    if b < 0:
+        raise MxqError("invalid sizes for rmsnorm_backward")
+    return b
+
+
+def rmsnorm_backward(grad_y: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
+                     grad_x: torch.Tensor, grad_weight: torch.Tensor, workspace: torch.Tensor,
+                     grad_res: torch.Tensor | None = None, stream=None) -> None:
+    """grad_y, h (the forward pass's res_out, or its x), grad_res bf16 (M, D); rstd fp32
+    (M,); grad_x bf16 (M, D) and grad_weight fp32 (D,) receive the gradients; workspace
+    uint8 of rmsnorm_backward_workspace_bytes(M, D)."""
+    M, D = _two(grad_y, "grad_y", "(M, D)")
+    n = M * D
+    a = _Args()
+    bf = torch.bfloat16
+    pg = a(grad_y, bf, "grad_y")
+    ph = a(h, bf, "h", n)
+    pw, ty = a.typed(weight, "weight", D)
+    pr = a(rstd, torch.float32, "rstd", M)
+    pe = a.optional(grad_res, bf, "grad_res", n)
+    po = a(grad_x, bf, "grad_x", n)
+    pd = a(grad_weight, torch.float32, "grad_weight", D)
+    ws = a(workspace, torch.uint8, "workspace")
+    if workspace.numel() < rmsnorm_backward_workspace_bytes(M, D):
+        raise MxqError("workspace is smaller than rmsnorm_backward_workspace_bytes")
+    a.run(lib().rmsnorm_backward, pg, ph, pw, ty, pr, pe, M, D, po, pd, ws, stream=stream)
+
+
+def mxfp4_quantize(x: torch.Tensor, q: torch.Tensor, s: torch.Tensor | None = None,
+                   sf_blocked: torch.Tensor | None = None, offs: torch.Tensor | None = None, stream=None) -> None:
+    """x bf16 (rows, cols) or (batch, rows, cols) -> q uint8 (.., cols/2) E2M1 code pairs,
+    with the E8M0 scales plain in s uint8 (.., cols/32), or in the tensor cores' tiles in
+    sf_blocked uint8 (mx_scales_blocked_bytes), or both; with offs (int32 end offsets) the
+    tiles are laid out per group, and rows in no group are left out."""
+    batch, rows, cols = _bsc(x)
+    n = batch * rows * cols
+    a = _Args()
+    px = a(x, torch.bfloat16, "x")
+    pq = a(q, torch.uint8, "q", n // 2)
+    ps = a.optional(s, torch.uint8, "s", n // 32)
+    pf = a.optional(sf_blocked, torch.uint8, "sf_blocked")
+    po = a.optional(offs, torch.int32, "offs")
+    G = 0 if offs is None else offs.numel()
+    if s is None and sf_blocked is None:
+        raise MxqError("mxfp4_quantize needs s or sf_blocked for the scales")
+    if offs is not None and (sf_blocked is None or G == 0):
+        raise MxqError("offs needs sf_blocked and at least one group")
+    if sf_blocked is not None and sf_blocked.numel() < mx_scales_blocked_bytes(batch, rows, cols // 32, G):
+        raise MxqError("sf_blocked is smaller than mx_scales_blocked_bytes")
+    a.run(lib().mxfp4_quantize, px, batch, rows, cols, pq, ps, pf, po, G, stream=stream)
+
+
+def mxfp4_dequantize(q: torch.Tensor, s: torch.Tensor, y: torch.Tensor, stream=None) -> None:
+    """q uint8 (.., cols/2) and s uint8 (.., cols/32) from mxfp4_quantize -> y bf16
+    (rows, cols) or (batch, rows, cols)."""
+    batch, rows, cols = _bsc(y)
+    n = batch * rows * cols
+    a = _Args()
+    pq = a(q, torch.uint8, "q", n // 2)
+    ps = a(s, torch.uint8, "s", n // 32)
+    py = a(y, torch.bfloat16, "y")
+    a.run(lib().mxfp4_dequantize, pq, ps, batch * rows, cols, py, stream=stream)
+
+
+def mxfp4_grouped_gemm(qa: torch.Tensor, sfa_blocked: torch.Tensor, qb: torch.Tensor, sfb_blocked: torch.Tensor,
+                       offs: torch.Tensor, out: torch.Tensor, stream=None) -> None:
+    """qa uint8 (M, K/2) tokens and sfa_blocked their scales, from mxfp4_quantize with offs;
+    qb uint8 (G, N, K/2) expert matrices and sfb_blocked their scales, from mxfp4_quantize;
+    offs int32 (G,) end offsets; out bf16 (M, N)."""
+    if qa.dim() != 2 or qb.dim() != 3:
+        raise MxqError("qa must be (M, K/2) and qb (G, N, K/2)")
+    M, Kb = qa.shape
+    G, N, Kb2 = qb.shape
+    if Kb2 != Kb or offs.numel() != G:
+        raise MxqError("qa, qb and offs disagree on K or G")
+    K = 2 * Kb
+    a = _Args()
+    pa = a(qa, torch.uint8, "qa")
+    pb = a(qb, torch.uint8, "qb")
+    psa = a(sfa_blocked, torch.uint8, "sfa_blocked")
+    psb = a(sfb_blocked, torch.uint8, "sfb_blocked")
+    if sfa_blocked.numel() < mx_scales_blocked_bytes(1, M, K // 32, G):
+        raise MxqError("sfa_blocked is smaller than mx_scales_blocked_bytes(1, M, K/32, G)")
+    if sfb_blocked.numel() < mx_scales_blocked_bytes(G, N, K // 32, 0):
+        raise MxqError("sfb_blocked is smaller than mx_scales_blocked_bytes(G, N, K/32, 0)")
+    po = a(offs, torch.int32, "offs")
+    pout = a(out, torch.bfloat16, "out", M * N)
+    a.run(lib().mxfp4_grouped_gemm, pa, psa, pb, psb, po, G, M, N, K, pout, stream=stream)

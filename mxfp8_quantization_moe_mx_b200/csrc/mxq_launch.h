@@ -67,6 +67,38 @@ cudaError_t launch_mx_grouped_gemm(const uint8_t* qa, const uint8_t* sfa, const 
                                    cudaStream_t stream);
 unsigned int read_gemm_timeouts();
 
+// MXFP4 quantize: plain scales s and / or (sf) scales in the block-scaled MMA's tiles, per
+// group with G > 0; dequantize n elements.
+cudaError_t launch_f4_quant(const uint16_t* x, int64_t batch, int64_t rows, int64_t cols, uint8_t* q, uint8_t* s,
+                            uint8_t* sf, const int32_t* offs, int32_t G, cudaStream_t stream);
+cudaError_t launch_f4_dequant(const uint8_t* q, const uint8_t* s, uint16_t* y, int64_t n, cudaStream_t stream);
+
+// MXFP4 grouped GEMM (tcgen05 kind::mxf4); scales in the blocked layout.
+cudaError_t launch_mxfp4_grouped_gemm(const uint8_t* qa, const uint8_t* sfa, const uint8_t* qb, const uint8_t* sfb,
+                                      const int32_t* offs, int32_t G, int64_t M, int64_t N, int64_t K, uint16_t* out,
+                                      cudaStream_t stream);
+unsigned int read_f4_gemm_timeouts();
+
+// Residual addition + RMS norm + MXFP8 (1x32) quantize, and the gradient of the norm.
+cudaError_t launch_rmsnorm_mx(const uint16_t* x, const uint16_t* residual, const void* w, bool w_bf16, int64_t M,
+                              int D, float eps, uint16_t* res_out, uint16_t* y, uint8_t* q, uint8_t* s, float* rstd,
+                              cudaStream_t stream);
+int64_t rmsnorm_workspace_bytes(int64_t M, int64_t D);
+cudaError_t launch_rmsnorm_backward(const uint16_t* gy, const uint16_t* h, const void* w, bool w_bf16,
+                                    const float* rstd, const uint16_t* gres, int64_t M, int D, uint16_t* gx,
+                                    float* gw, float* ws, cudaStream_t stream);
+
+// Routing of tokens to experts, its gradient, and the rows of the routed slots.
+cudaError_t launch_moe_route(const void* logits, bool bf16, int64_t T, int E, const float* bias, int score,
+                             int n_groups, int top_groups, int group_top, int k, bool renorm, float scale,
+                             float* weights, int32_t* ids, cudaStream_t stream);
+cudaError_t launch_moe_route_backward(const void* logits, bool bf16, int64_t T, int E, const int32_t* ids, int k,
+                                      const float* grad_weights, int score, bool renorm, float scale,
+                                      void* grad_logits, cudaStream_t stream);
+int64_t plan_workspace_bytes(int64_t n, int E);
+cudaError_t launch_moe_plan(const int32_t* ids, int64_t n, int E, int32_t* offs, int32_t* rows, int32_t* src,
+                            int32_t* ws, cudaStream_t stream);
+
 // Number of per-group CTAs that gave up a bounded wait, and of those whose copies in
 // flight did not land within the drain limit either (synchronous reads).
 unsigned int read_wait_timeouts();
