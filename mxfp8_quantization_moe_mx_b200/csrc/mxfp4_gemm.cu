@@ -19,8 +19,8 @@
 //           HBM.  Only the 8- or 32-row pieces of the token tile that hold rows of the group
 //           are loaded.  A unit's tokens always begin a 128-row scale tile: the MMA takes a
 //           scale address only at the first of a tile's four tensor-memory columns.
-// Both are persistent, with one producer lane (TMA), one MMA lane, four epilogue warps, and
-// every wait bounded as in the MXFP8 kernel (mxq_wait_timeouts counts CTAs that gave up).
+// Both are persistent, with a producer warp (TMA), an MMA warp, four epilogue warps, and every
+// wait bounded as in the MXFP8 kernel (mxq_wait_timeouts counts CTAs that gave up).
 
 #include <algorithm>
 #include <cstring>
@@ -49,9 +49,14 @@ constexpr int FW_OFF_SFA = FW_OFF_B + FW_STAGES * F4_TILE;
 constexpr int FW_OFF_SFB = FW_OFF_SFA + FW_STAGES * F4_SF;
 constexpr int FW_SMEM = FW_OFF_SFB + FW_STAGES * 2 * F4_SF + 1024;  // + alignment slack
 constexpr uint32_t FW_CTA_TX = 2 * F4_TILE + 3 * F4_SF;             // one CTA's bytes per stage
-constexpr uint32_t FW_TMEM_SFA = 256;                               // 8 columns per stage
-constexpr uint32_t FW_TMEM_SFB = 256 + 8 * FW_STAGES;               // 16 columns per stage
-static_assert(FW_TMEM_SFB + 16 * FW_STAGES <= 512, "tensor-memory columns");
+// Tensor memory: two accumulators of 256 columns that share 64, and two slots of 8 + 16
+// scale columns.  A unit's epilogue reads the shared columns first, so the next unit's MMAs
+// wait for a quarter of it.
+constexpr uint32_t FW_ACC1 = 192;
+constexpr uint32_t FW_SHARED = 64;
+constexpr uint32_t FW_TMEM_SF = 448;
+static_assert(FW_ACC1 + FW_SHARED == FW_BN && FW_ACC1 + FW_BN == FW_TMEM_SF && FW_TMEM_SF + 2 * 24 <= 512,
+              "tensor-memory columns");
 static_assert(FW_SMEM <= 227 * 1024, "shared memory per CTA");
 
 __device__ __forceinline__ void mma_f4_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
@@ -65,6 +70,22 @@ __device__ __forceinline__ void mma_f4_pair(uint32_t d_tmem, uint64_t adesc, uin
         : "memory");
 }
 
+// One lane of the (converged) warp.  The producer and MMA warps walk their units with all
+// lanes and let an elected lane issue: descriptors, addresses and loop state then stay in
+// uniform registers, which the TMA and MMA instructions take them from.  Issued by one lane
+// of a diverged warp instead, an MMA took about twice its own time to issue (20 K blocks of
+// a 256 x 256 unit: 0.71 us each against 0.56).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// A wait of the whole warp with one outcome.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+    return __all_sync(FULL_MASK, mbar_wait_bounded(bar, parity, GG_WAIT_NS));
+}
+
 // Instruction descriptor of kind::mxf4: E2M1 A and B, E8M0 scales, an M x N tile; `id` the
 // first of the two scale bytes (0 or 2) of the A and B scale columns.
 template <int M>
@@ -72,6 +93,20 @@ __device__ __forceinline__ uint32_t idesc_f4(uint32_t n, uint32_t id) {
     constexpr uint32_t base = 1u << 7 | 1u << 10 | 1u << 23 | (uint32_t)(M >> 4) << 24;
     return base | (n >> 3) << 17 | id << 4 | id << 29;
 }
+
+// 32 consecutive fp32 columns of this warp's 32 tensor-memory lanes into v[0..31], which hold
+// them once tmem_wait_ld has returned.
+__device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, uint32_t* v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+          "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1) f4_gemm_wide_kernel(
     const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
@@ -90,7 +125,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1) f4_gemm_wide
     const bool first = rank == 0;
     const int64_t cl = blockIdx.x >> 1, n_cl = gridDim.x >> 1;
     const int64_t n_tiles_n = N / FW_BN;
-    const int64_t k_blocks = (K + F4_BK - 1) / F4_BK;
     const int64_t col_tiles = K / 128;
 
     if (warp == 0) {
@@ -119,125 +153,150 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1) f4_gemm_wide
     const uint32_t full0 = cluster_map(&full[0], 0);  // the first CTA's `full` ring (8 bytes apart)
     const uint32_t acc_empty0 = cluster_map(&acc_empty, 0);
 
+    const int k_full = (int)(K / F4_BK), k_half = (int)(K % F4_BK != 0);
     uint32_t it_prod = 0;
     if (warp == 0) {
         // ---- producer (both CTAs)
         const uint64_t pol = l2_policy_evict_last();
-        bool stop = false;
-        for (int64_t w = cl; w < n_work && !stop; w += n_cl) {
+        const bool el = elect_one();
+        uint32_t s = 0, ph = 1;
+        bool ok = true;
+        for (int64_t w = cl; w < n_work && ok; w += n_cl) {
             const int64_t p = w / n_tiles_n, n0 = (w % n_tiles_n) * FW_BN;
             PairTile pt;
             gg_find_pair(offs, G, M, p, &pt, nullptr);
-            if (lane == 0) {
-                const int64_t my_row = pt.row0 + (int64_t)rank * F4_ROWS;
-                const int64_t my_mt = (rank == 1 && pt.valid1 > 0) ? pt.mt0 + 1 : pt.mt0;  // filler: any real tile
-                const int64_t sfa_row = 2 * my_mt * col_tiles;
-                const int64_t sfb_row = 2 * ((int64_t)pt.g * (N / 128) + n0 / 128) * col_tiles;
-                const int b_row = (int)((int64_t)pt.g * N + n0 + (int64_t)rank * (FW_BN / 2));
-                for (int64_t kb = 0; kb < k_blocks; ++kb, ++it_prod) {
-                    const int s = (int)(it_prod % FW_STAGES);
-                    const uint32_t r = it_prod / FW_STAGES;
-                    if (!mbar_wait_bounded(&empty[s], (r & 1) ^ 1, GG_WAIT_NS) || *(volatile int*)&abort_s) {
-                        atomicExch(&abort_s, 1);
-                        stop = true;
-                        break;
-                    }
+            const int my_row = (int)(pt.row0 + (int64_t)rank * F4_ROWS);
+            const int64_t my_mt = (rank == 1 && pt.valid1 > 0) ? pt.mt0 + 1 : pt.mt0;  // filler: any real tile
+            int sfa_row = (int)(2 * my_mt * col_tiles);
+            int sfb_row = (int)(2 * ((int64_t)pt.g * (N / 128) + n0 / 128) * col_tiles);
+            const int sfb_half = (int)(2 * col_tiles);
+            const int b_row = (int)((int64_t)pt.g * N + n0 + (int64_t)rank * (FW_BN / 2));
+            for (int kb = 0; kb < k_full + k_half; ++kb, ++it_prod, sfa_row += 4, sfb_row += 4) {
+                if (!warp_wait(&empty[s], ph) || *(volatile int*)&abort_s) {
+                    ok = false;
+                    break;
+                }
+                if (el) {
                     if (first) mbar_arrive_expect_tx(&full[s], 2 * FW_CTA_TX);
-                    const uint32_t bar = full0 + 8u * (uint32_t)s;
-                    tma_load_2d_pair(sm + s * F4_TILE, &amap, (int)(kb * F4_BKB), (int)my_row, bar, pol);
-                    tma_load_2d_pair(sm + FW_OFF_B + s * F4_TILE, &bmap, (int)(kb * F4_BKB), b_row, bar, pol);
-                    tma_load_2d_pair(sm + FW_OFF_SFA + s * F4_SF, &sfamap, 0, (int)(sfa_row + 4 * kb), bar, pol);
-                    tma_load_2d_pair(sm + FW_OFF_SFB + s * 2 * F4_SF, &sfbmap, 0, (int)(sfb_row + 4 * kb), bar, pol);
-                    tma_load_2d_pair(sm + FW_OFF_SFB + s * 2 * F4_SF + F4_SF, &sfbmap, 0,
-                                     (int)(sfb_row + 2 * col_tiles + 4 * kb), bar, pol);
+                    const uint32_t bar = full0 + 8u * s;
+                    tma_load_2d_pair(sm + s * F4_TILE, &amap, kb * F4_BKB, my_row, bar, pol);
+                    tma_load_2d_pair(sm + FW_OFF_B + s * F4_TILE, &bmap, kb * F4_BKB, b_row, bar, pol);
+                    tma_load_2d_pair(sm + FW_OFF_SFA + s * F4_SF, &sfamap, 0, sfa_row, bar, pol);
+                    tma_load_2d_pair(sm + FW_OFF_SFB + s * 2 * F4_SF, &sfbmap, 0, sfb_row, bar, pol);
+                    tma_load_2d_pair(sm + FW_OFF_SFB + s * 2 * F4_SF + F4_SF, &sfbmap, 0, sfb_row + sfb_half, bar,
+                                     pol);
+                }
+                if (++s == FW_STAGES) {
+                    s = 0;
+                    ph ^= 1;
                 }
             }
-            stop = __shfl_sync(FULL_MASK, stop ? 1 : 0, 0) != 0;
         }
+        if (!ok && el) atomicExch(&abort_s, 1);
         __syncwarp();
     } else if (warp == 1) {
         // ---- MMA issuer (the first CTA)
-        if (first && lane == 0) {
-            uint32_t it = 0;
-            int64_t i = 0;
-            for (int64_t w = cl; w < n_work; w += n_cl, ++i) {
-                if (i > 0 && !mbar_wait_bounded(&acc_empty, (uint32_t)((i - 1) & 1), GG_WAIT_NS)) {
-                    atomicExch(&abort_s, 1);
-                    break;
-                }
+        if (first) {
+            const bool el = elect_one();
+            const uint64_t a_base = desc_sw128(sm), b_base = desc_sw128(sm + FW_OFF_B);
+            const uint64_t sfa_base = desc_sf(sm + FW_OFF_SFA), sfb_base = desc_sf(sm + FW_OFF_SFB);
+            constexpr uint32_t T = F4_TILE / 16, SF = F4_SF / 16;  // descriptor units of 16 bytes
+            uint32_t s = 0, ph = 0, slot = 0, unit = 0;
+            bool ok = true;
+            for (int64_t w = cl; w < n_work; w += n_cl, ++unit) {
+                if (unit > 0 && !warp_wait(&acc_empty, (unit - 1) & 1)) ok = false;
+                if (!ok) break;
                 tc_fence_after();
-                bool ok = true;
-                for (int64_t kb = 0; kb < k_blocks; ++kb, ++it) {
-                    const int s = (int)(it % FW_STAGES);
-                    const uint32_t r = it / FW_STAGES;
-                    if (!mbar_wait_bounded(&full[s], r & 1, GG_WAIT_NS) || *(volatile int*)&abort_s) {
-                        atomicExch(&abort_s, 1);
+                const uint32_t acc = tmem + (unit & 1 ? FW_ACC1 : 0);
+                for (int kb = 0; kb < k_full + k_half; ++kb) {
+                    if (!warp_wait(&full[s], ph)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    // scale columns: A [scale tile][4], B [scale tile][column half][4]
-                    const uint32_t t_sfa = tmem + FW_TMEM_SFA + 8 * s, t_sfb = tmem + FW_TMEM_SFB + 16 * s;
-                    const uint8_t* sfa = sm + FW_OFF_SFA + s * F4_SF;
-                    const uint8_t* sfb = sm + FW_OFF_SFB + s * 2 * F4_SF;
-                    tmem_cp_sf_pair(t_sfa, desc_sf(sfa));
-                    tmem_cp_sf_pair(t_sfb, desc_sf(sfb));
-                    tmem_cp_sf_pair(t_sfb + 4, desc_sf(sfb + F4_SF));
-                    tmem_cp_sf_pair(t_sfa + 4, desc_sf(sfa + 512));
-                    tmem_cp_sf_pair(t_sfb + 8, desc_sf(sfb + 512));
-                    tmem_cp_sf_pair(t_sfb + 12, desc_sf(sfb + F4_SF + 512));
-                    const uint64_t a0 = desc_sw128(sm + s * F4_TILE), b0 = desc_sw128(sm + FW_OFF_B + s * F4_TILE);
-                    const uint32_t nk = K - kb * F4_BK >= F4_BK ? 4 : 2;
-                    for (uint32_t k = 0; k < nk; ++k) {  // K = 64 per MMA: 32 bytes further along the swizzled rows
-                        const uint32_t id = 2 * (k & 1), t = k >> 1;
-                        mma_f4_pair(tmem, a0 + 2 * k, b0 + 2 * k, idesc_f4<256>(FW_BN, id),
-                                    (t_sfa + 4 * t) | id << 30, (t_sfb + 8 * t) | id << 30,
-                                    (kb > 0 || k > 0) ? 1u : 0u);
+                    if (el) {
+                        // scale columns: A [scale tile][4], B [scale tile][column half][4]; copies
+                        // and MMAs of one thread run in order, so two slots are enough
+                        const uint32_t t_a = tmem + FW_TMEM_SF + 24 * slot, t_b = t_a + 8;
+                        const uint64_t sfa = sfa_base + s * SF, sfb = sfb_base + s * 2 * SF;
+                        const uint64_t a0 = a_base + s * T, b0 = b_base + s * T;
+                        tmem_cp_sf_pair(t_a, sfa);
+                        tmem_cp_sf_pair(t_b, sfb);
+                        tmem_cp_sf_pair(t_b + 4, sfb + SF);
+                        tmem_cp_sf_pair(t_a + 4, sfa + SF / 2);
+                        tmem_cp_sf_pair(t_b + 8, sfb + SF / 2);
+                        tmem_cp_sf_pair(t_b + 12, sfb + SF + SF / 2);
+                        // K = 64 per MMA: 32 bytes further along the swizzled rows
+                        constexpr uint32_t HI = 2u << 30;  // the upper two scale bytes of a column
+                        mma_f4_pair(acc, a0, b0, idesc_f4<256>(FW_BN, 0), t_a, t_b, kb > 0);
+                        mma_f4_pair(acc, a0 + 2, b0 + 2, idesc_f4<256>(FW_BN, 2), t_a | HI, t_b | HI, 1);
+                        if (kb < k_full) {
+                            mma_f4_pair(acc, a0 + 4, b0 + 4, idesc_f4<256>(FW_BN, 0), t_a + 4, t_b + 8, 1);
+                            mma_f4_pair(acc, a0 + 6, b0 + 6, idesc_f4<256>(FW_BN, 2), (t_a + 4) | HI, (t_b + 8) | HI,
+                                        1);
+                        }
+                        mma_commit_both(&empty[s]);  // the stage is free in both CTAs once these have read it
+                        if (kb == k_full + k_half - 1) mma_commit_both(&acc_full);
                     }
-                    mma_commit_both(&empty[s]);  // the stage is free in both CTAs once these MMAs have read it
+                    __syncwarp();
+                    slot ^= 1;
+                    if (++s == FW_STAGES) {
+                        s = 0;
+                        ph ^= 1;
+                    }
                 }
-                if (!ok) break;              // a partial accumulator is never handed to the epilogues
-                mma_commit_both(&acc_full);  // the unit's accumulators are complete once its MMAs are
+                if (!ok) break;  // a partial accumulator is never handed to the epilogues
             }
             // every tcgen05 operation issued above (and its arrivals) is done before the pair
             // frees tensor memory or leaves
-            mma_commit_own(&drained);
-            if (!mbar_wait_bounded(&drained, 0, GG_DRAIN_NS)) atomicExch(&abort_s, 1);
+            if (el) {
+                if (!ok) atomicExch(&abort_s, 1);
+                mma_commit_own(&drained);
+                if (!mbar_wait_bounded(&drained, 0, GG_DRAIN_NS)) atomicExch(&abort_s, 1);
+            }
         }
         __syncwarp();
     } else {
         // ---- epilogue (both CTAs): warp w reads accumulator lanes (rows) 32 (w % 4) .. + 31
         const int quarter = warp & 3;
         const int r = 32 * quarter + lane;
-        int64_t i = 0;
-        for (int64_t w = cl; w < n_work; w += n_cl, ++i) {
+        uint32_t unit = 0;
+        for (int64_t w = cl; w < n_work; w += n_cl, ++unit) {
             const int64_t p = w / n_tiles_n, n0 = (w % n_tiles_n) * FW_BN;
             PairTile pt;
             gg_find_pair(offs, G, M, p, &pt, nullptr);
-            const bool done = mbar_wait_bounded(&acc_full, (uint32_t)(i & 1), GG_WAIT_NS);
+            const bool done = mbar_wait_bounded(&acc_full, unit & 1, GG_WAIT_NS);
             if (!done) atomicExch(&abort_s, 1);
             if (__any_sync(FULL_MASK, !done) || *(volatile int*)&abort_s) break;
             tc_fence_after();
-            // the whole row, rounded to bf16 in registers, so the accumulator is released
-            // before the stores and the next unit's MMAs overlap them
-            uint32_t v16[FW_BN / 2];
+            const uint32_t acc = tmem + (unit & 1 ? FW_ACC1 : 0) + ((uint32_t)(32 * quarter) << 16);
+            // the shared columns first: the last of the even units' accumulator, the first of
+            // the odd units'
+            const int c_first = unit & 1 ? 0 : FW_BN - (int)FW_SHARED;
+            const bool live = r < (rank == 0 ? pt.valid0 : pt.valid1);
+            uint16_t* orow = out + (pt.row0 + (int64_t)rank * F4_ROWS + r) * N + n0;
+#pragma unroll 1
+            for (int i = 0; i < FW_BN / 64; ++i) {
+                const int c0 = (c_first + 64 * i) & (FW_BN - 1);
+                uint32_t v[64];
+                tmem_ld32_nowait(acc + (uint32_t)c0, v);
+                tmem_ld32_nowait(acc + (uint32_t)c0 + 32, v + 32);
+                tmem_wait_ld();
+                if (i == 0) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(acc_empty0);  // this warp's shared columns are read
+                }
+                if (live) {
 #pragma unroll
-            for (int c0 = 0; c0 < FW_BN; c0 += 32) {
-                uint32_t v[32];
-                tmem_ld32(tmem + ((uint32_t)(32 * quarter) << 16) + (uint32_t)c0, v);
+                    for (int q = 0; q < 8; ++q) {
+                        uint32_t o[4];
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    v16[c0 / 2 + j] = cvt_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(acc_empty0);  // this warp's quarter is read
-            const int64_t valid = rank == 0 ? pt.valid0 : pt.valid1;
-            if (r < valid) {
-                uint4* orow = reinterpret_cast<uint4*>(out + (pt.row0 + (int64_t)rank * F4_ROWS + r) * N + n0);
-#pragma unroll
-                for (int q = 0; q < FW_BN / 8; ++q)
-                    orow[q] = make_uint4(v16[4 * q], v16[4 * q + 1], v16[4 * q + 2], v16[4 * q + 3]);
+                        for (int j = 0; j < 4; ++j)
+                            o[j] = cvt_bf16x2(__uint_as_float(v[8 * q + 2 * j]), __uint_as_float(v[8 * q + 2 * j + 1]));
+                        *reinterpret_cast<uint4*>(orow + c0 + 8 * q) = make_uint4(o[0], o[1], o[2], o[3]);
+                    }
+                }
             }
         }
     }
@@ -276,8 +335,7 @@ constexpr int FN_OFF_T = FN_STAGES * F4_TILE;
 constexpr int FN_OFF_SFW = FN_OFF_T + FN_STAGES * F4_TILE;
 constexpr int FN_OFF_SFT = FN_OFF_SFW + FN_STAGES * F4_SF;
 constexpr int FN_SMEM = FN_OFF_SFT + FN_STAGES * F4_SF + 1024;
-constexpr uint32_t FN_TMEM_SF = 256;  // after two accumulators of 128 columns: 16 columns per stage
-static_assert(FN_TMEM_SF + 16 * FN_STAGES <= 512, "tensor-memory columns");
+constexpr uint32_t FN_TMEM_SF = 256;  // after two accumulators of 128 columns: two slots of 16 columns
 static_assert(FN_SMEM <= 214 * 1024, "shared memory per CTA, with the table of the groups");
 
 constexpr int FN_MAX_G = 1024;  // groups whose first tiles are kept in shared memory
@@ -389,7 +447,6 @@ __global__ void __launch_bounds__(192, 1) f4_gemm_narrow_kernel(
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t n_w = N / F4_ROWS;  // weight tiles of a group
-    const int64_t k_blocks = (K + F4_BK - 1) / F4_BK;
     const int64_t col_tiles = K / 128;
 
     if (warp == 0) {
@@ -420,81 +477,96 @@ __global__ void __launch_bounds__(192, 1) f4_gemm_narrow_kernel(
     const uint32_t tmem = tmem_base_s;
     const int64_t n_work = n_tiles_s * n_w;
 
+    const int k_full = (int)(K / F4_BK), k_half = (int)(K % F4_BK != 0);
     uint32_t it_prod = 0;
     if (warp == 0) {
-        if (lane == 0) {
-            const uint64_t keep = l2_policy_evict_last(), once = l2_policy_evict_first();
-            bool stop = false;
-            for (int64_t w = blockIdx.x; w < n_work && !stop; w += gridDim.x) {
-                const TokenTile tt = find_tile(tab, G, (int)(w / n_w));
-                const int64_t n0 = (w % n_w) * F4_ROWS;
-                // up to 24 tokens in pieces of 8 rows, more in pieces of 32
-                const int box = tt.valid <= 24 ? 8 : 32;
-                const CUtensorMap* tm = tt.valid <= 24 ? &tmap8 : &tmap;
-                const int pieces = (tt.valid + box - 1) / box;
-                const uint32_t tx = F4_TILE + 2 * F4_SF + (uint32_t)(pieces * box * F4_BKB);
-                const int64_t sft_row = 2 * (int64_t)tt.mt * col_tiles;
-                const int64_t sfw_row = 2 * ((int64_t)tt.g * n_w + n0 / 128) * col_tiles;
-                const int w_row = (int)((int64_t)tt.g * N + n0);
-                for (int64_t kb = 0; kb < k_blocks; ++kb, ++it_prod) {
-                    const int s = (int)(it_prod % S);
-                    const uint32_t r = it_prod / S;
-                    if (!mbar_wait_bounded(&empty[s], (r & 1) ^ 1, GG_WAIT_NS) || *(volatile int*)&abort_s) {
-                        atomicExch(&abort_s, 1);
-                        stop = true;
-                        break;
-                    }
+        const uint64_t keep = l2_policy_evict_last(), once = l2_policy_evict_first();
+        const bool el = elect_one();
+        uint32_t s = 0, ph = 1;
+        bool ok = true;
+        for (int64_t w = blockIdx.x; w < n_work && ok; w += gridDim.x) {
+            const TokenTile tt = find_tile(tab, G, (int)(w / n_w));
+            const int64_t n0 = (w % n_w) * F4_ROWS;
+            // up to 24 tokens in pieces of 8 rows, more in pieces of 32
+            const int box = tt.valid <= 24 ? 8 : 32;
+            const CUtensorMap* tm = tt.valid <= 24 ? &tmap8 : &tmap;
+            const int pieces = (tt.valid + box - 1) / box;
+            const uint32_t tx = F4_TILE + 2 * F4_SF + (uint32_t)(pieces * box * F4_BKB);
+            int sft_row = (int)(2 * (int64_t)tt.mt * col_tiles);
+            int sfw_row = (int)(2 * ((int64_t)tt.g * n_w + n0 / 128) * col_tiles);
+            const int w_row = (int)((int64_t)tt.g * N + n0), t_row = (int)tt.row0;
+            for (int kb = 0; kb < k_full + k_half; ++kb, ++it_prod, sft_row += 4, sfw_row += 4) {
+                if (!warp_wait(&empty[s], ph) || *(volatile int*)&abort_s) {
+                    ok = false;
+                    break;
+                }
+                if (el) {
                     mbar_arrive_expect_tx(&full[s], tx);
-                    tma_load_2d(sm + s * F4_TILE, &wmap, (int)(kb * F4_BKB), w_row, &full[s], once);
-                    tma_load_2d(sm + FN_OFF_SFW + s * F4_SF, &sfwmap, 0, (int)(sfw_row + 4 * kb), &full[s], once);
+                    tma_load_2d(sm + s * F4_TILE, &wmap, kb * F4_BKB, w_row, &full[s], once);
+                    tma_load_2d(sm + FN_OFF_SFW + s * F4_SF, &sfwmap, 0, sfw_row, &full[s], once);
                     for (int p = 0; p < pieces; ++p)
-                        tma_load_2d(sm + FN_OFF_T + s * F4_TILE + p * box * F4_BKB, tm, (int)(kb * F4_BKB),
-                                    (int)tt.row0 + p * box, &full[s], keep);
-                    tma_load_2d(sm + FN_OFF_SFT + s * F4_SF, &sftmap, 0, (int)(sft_row + 4 * kb), &full[s], keep);
+                        tma_load_2d(sm + FN_OFF_T + s * F4_TILE + p * box * F4_BKB, tm, kb * F4_BKB, t_row + p * box,
+                                    &full[s], keep);
+                    tma_load_2d(sm + FN_OFF_SFT + s * F4_SF, &sftmap, 0, sft_row, &full[s], keep);
+                }
+                if (++s == S) {
+                    s = 0;
+                    ph ^= 1;
                 }
             }
         }
+        if (!ok && el) atomicExch(&abort_s, 1);
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0) {
-            uint32_t it = 0;
-            int64_t i = 0;
-            for (int64_t w = blockIdx.x; w < n_work; w += gridDim.x, ++i) {
-                const uint32_t cols = (uint32_t)(find_tile(tab, G, (int)(w / n_w)).valid + 31) / 32 * 32;
-                const int buf = (int)(i & 1);
-                if (i > 1 && !mbar_wait_bounded(&acc_empty[buf], (uint32_t)((i / 2 - 1) & 1), GG_WAIT_NS)) {
-                    atomicExch(&abort_s, 1);
+        const bool el = elect_one();
+        const uint64_t w_base = desc_sw128(sm), t_base = desc_sw128(sm + FN_OFF_T);
+        const uint64_t sfw_base = desc_sf(sm + FN_OFF_SFW), sft_base = desc_sf(sm + FN_OFF_SFT);
+        constexpr uint32_t T = F4_TILE / 16, SF = F4_SF / 16;  // descriptor units of 16 bytes
+        uint32_t s = 0, ph = 0, slot = 0, unit = 0;
+        bool ok = true;
+        for (int64_t w = blockIdx.x; w < n_work; w += gridDim.x, ++unit) {
+            const uint32_t cols = (uint32_t)(find_tile(tab, G, (int)(w / n_w)).valid + 31) / 32 * 32;
+            const uint32_t buf = unit & 1;
+            if (unit > 1 && !warp_wait(&acc_empty[buf], (unit / 2 - 1) & 1)) ok = false;
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t acc = tmem + buf * 128;
+            const uint32_t id0 = idesc_f4<128>(cols, 0), id2 = idesc_f4<128>(cols, 2);
+            for (int kb = 0; kb < k_full + k_half; ++kb) {
+                if (!warp_wait(&full[s], ph)) {
+                    ok = false;
                     break;
                 }
                 tc_fence_after();
-                bool ok = true;
-                for (int64_t kb = 0; kb < k_blocks; ++kb, ++it) {
-                    const int s = (int)(it % S);
-                    if (!mbar_wait_bounded(&full[s], (it / S) & 1, GG_WAIT_NS) || *(volatile int*)&abort_s) {
-                        atomicExch(&abort_s, 1);
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t t_w = tmem + FN_TMEM_SF + 16 * s, t_t = t_w + 8;
-                    const uint8_t* sfw = sm + FN_OFF_SFW + s * F4_SF;
-                    const uint8_t* sft = sm + FN_OFF_SFT + s * F4_SF;
-                    tmem_cp_sf(t_w, desc_sf(sfw));
-                    tmem_cp_sf(t_w + 4, desc_sf(sfw + 512));
-                    tmem_cp_sf(t_t, desc_sf(sft));
-                    tmem_cp_sf(t_t + 4, desc_sf(sft + 512));
-                    const uint64_t a0 = desc_sw128(sm + s * F4_TILE), b0 = desc_sw128(sm + FN_OFF_T + s * F4_TILE);
-                    const uint32_t nk = K - kb * F4_BK >= F4_BK ? 4 : 2;
-                    for (uint32_t k = 0; k < nk; ++k) {
-                        const uint32_t id = 2 * (k & 1), t = k >> 1;
-                        mma_f4(tmem + buf * 128, a0 + 2 * k, b0 + 2 * k, idesc_f4<128>(cols, id),
-                               (t_w + 4 * t) | id << 30, (t_t + 4 * t) | id << 30, (kb > 0 || k > 0) ? 1u : 0u);
+                if (el) {
+                    const uint32_t t_w = tmem + FN_TMEM_SF + 16 * slot, t_t = t_w + 8;
+                    const uint64_t sfw = sfw_base + s * SF, sft = sft_base + s * SF;
+                    const uint64_t a0 = w_base + s * T, b0 = t_base + s * T;
+                    tmem_cp_sf(t_w, sfw);
+                    tmem_cp_sf(t_t, sft);
+                    tmem_cp_sf(t_w + 4, sfw + SF / 2);
+                    tmem_cp_sf(t_t + 4, sft + SF / 2);
+                    constexpr uint32_t HI = 2u << 30;
+                    mma_f4(acc, a0, b0, id0, t_w, t_t, kb > 0);
+                    mma_f4(acc, a0 + 2, b0 + 2, id2, t_w | HI, t_t | HI, 1);
+                    if (kb < k_full) {
+                        mma_f4(acc, a0 + 4, b0 + 4, id0, t_w + 4, t_t + 4, 1);
+                        mma_f4(acc, a0 + 6, b0 + 6, id2, (t_w + 4) | HI, (t_t + 4) | HI, 1);
                     }
                     mma_commit(&empty[s]);
+                    if (kb == k_full + k_half - 1) mma_commit(&acc_full[buf]);
                 }
-                if (!ok) break;
-                mma_commit(&acc_full[buf]);
+                __syncwarp();
+                slot ^= 1;
+                if (++s == S) {
+                    s = 0;
+                    ph ^= 1;
+                }
             }
+            if (!ok) break;
+        }
+        if (el) {
+            if (!ok) atomicExch(&abort_s, 1);
             mma_commit(&drained);
             if (!mbar_wait_bounded(&drained, 0, GG_DRAIN_NS)) atomicExch(&abort_s, 1);
         }
