@@ -314,38 +314,57 @@ def mx_grouped_gemm(qa: torch.Tensor, sfa_blocked: torch.Tensor, qb: torch.Tenso
 
 # ---- the operators of a mixture-of-experts layer --------------------------------------------------
 
-class _Args:
-    """The pointers of one call's tensors, which have to lie on one CUDA device."""
+def _refuse(t, dtype, name: str, numel, dev: int) -> None:
+    """Raise what is wrong with an argument that _arg has not accepted."""
+    _dev(t, dtype, name, numel)
+    raise MxqError(f"{name} is on {t.device}, the other tensors are on cuda:{dev}")
 
-    __slots__ = ("device",)
 
-    def __init__(self):
-        self.device = None
+def _arg(t: torch.Tensor, dtype, name: str, numel: int, dev: int) -> int:
+    """The pointer of a contiguous tensor of numel elements on CUDA device dev."""
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.numel() == numel and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, dtype, name, numel, dev)
 
-    def __call__(self, t: torch.Tensor, dtype, name: str, numel: int | None = None) -> int:
-        p = _dev(t, dtype, name, numel)
-        if self.device is None:
-            self.device = t.device
-        elif t.device != self.device:
-            raise MxqError(f"{name} is on {t.device}, the other tensors are on {self.device}")
-        return p
 
-    def optional(self, t, dtype, name: str, numel: int | None = None):
-        return None if t is None else self(t, dtype, name, numel)
+def _opt(t, dtype, name: str, numel: int, dev: int):
+    return None if t is None else _arg(t, dtype, name, numel, dev)
 
-    def typed(self, t: torch.Tensor, name: str, numel: int | None = None) -> tuple[int, int]:
-        """(pointer, type code) of a bf16 or fp32 tensor."""
-        if isinstance(t, torch.Tensor) and t.dtype == torch.float32:
-            return self(t, torch.float32, name, numel), 1
-        return self(t, torch.bfloat16, name, numel), 0
 
-    def run(self, f, *args, stream=None) -> None:
-        """f(*args, stream) on the tensors' device: on its current stream unless one is given."""
-        if self.device.index == torch.cuda.current_device():
-            _check(f(*args, _stream(stream)))
-        else:
-            with torch.cuda.device(self.device):
-                _check(f(*args, _stream(stream)))
+def _first(t: torch.Tensor, name: str) -> int:
+    """The device of a call: that of its first tensor."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise MxqError(f"{name} must be a CUDA tensor")
+    return t.get_device()
+
+
+def _type_of(t, name: str) -> int:
+    d = getattr(t, "dtype", None)
+    if d is torch.bfloat16:
+        return 0
+    if d is torch.float32:
+        return 1
+    raise MxqError(f"{name} must be a bfloat16 or float32 tensor")
+
+
+_DTYPES = (torch.bfloat16, torch.float32)
+_RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _run(f, dev: int, stream, *args) -> None:
+    """f(*args, stream) on device dev: on its current stream unless one is given."""
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            status = f(*args, _stream(stream))
+    elif stream is None and _RAW_STREAM is not None:
+        status = f(*args, _RAW_STREAM(dev))
+    else:
+        status = f(*args, _stream(stream))
+    if status:
+        _check(status)
 
 
 def _two(t: torch.Tensor, name: str, what: str) -> tuple[int, int]:
@@ -361,13 +380,10 @@ def moe_route(logits: torch.Tensor, weights: torch.Tensor, ids: torch.Tensor, bi
     (T, k) receive the k experts of each token and their weights."""
     T, E = _two(logits, "logits", "(T, E)")
     k = _two(ids, "ids", "(T, k)")[1]
-    a = _Args()
-    pl, ty = a.typed(logits, "logits")
-    pb = a.optional(bias, torch.float32, "bias", E)
-    pw = a(weights, torch.float32, "weights", T * k)
-    pi = a(ids, torch.int32, "ids", T * k)
-    a.run(lib().moe_route, pl, ty, T, E, pb, score, n_groups, top_groups, group_top, k, bool(renorm), scale, pw, pi,
-          stream=stream)
+    dev, ty = _first(logits, "logits"), _type_of(logits, "logits")
+    _run(lib().moe_route, dev, stream, _arg(logits, _DTYPES[ty], "logits", T * E, dev), ty, T, E,
+         _opt(bias, torch.float32, "bias", E, dev), score, n_groups, top_groups, group_top, k, 1 if renorm else 0,
+         scale, _arg(weights, torch.float32, "weights", T * k, dev), _arg(ids, torch.int32, "ids", T * k, dev))
 
 
 def moe_route_backward(logits: torch.Tensor, ids: torch.Tensor, grad_weights: torch.Tensor,
@@ -377,16 +393,14 @@ def moe_route_backward(logits: torch.Tensor, ids: torch.Tensor, grad_weights: to
     (T, k), grad_logits (T, E) of the logits' type (written whole)."""
     T, E = _two(logits, "logits", "(T, E)")
     k = _two(ids, "ids", "(T, k)")[1]
-    a = _Args()
-    pl, ty = a.typed(logits, "logits")
-    pi = a(ids, torch.int32, "ids", T * k)
-    pg = a(grad_weights, torch.float32, "grad_weights", T * k)
-    po = a(grad_logits, logits.dtype, "grad_logits", T * E)
-    a.run(lib().moe_route_backward, pl, ty, T, E, pi, k, pg, score, bool(renorm), scale, po, stream=stream)
+    dev, ty = _first(logits, "logits"), _type_of(logits, "logits")
+    _run(lib().moe_route_backward, dev, stream, _arg(logits, _DTYPES[ty], "logits", T * E, dev), ty, T, E,
+         _arg(ids, torch.int32, "ids", T * k, dev), k, _arg(grad_weights, torch.float32, "grad_weights", T * k, dev),
+         score, 1 if renorm else 0, scale, _arg(grad_logits, _DTYPES[ty], "grad_logits", T * E, dev))
 
 
 def moe_plan_workspace_bytes(n: int, E: int) -> int:
-    b = int(lib().moe_plan_workspace_bytes(n, E))
+    b = lib().moe_plan_workspace_bytes(n, E)
     if b < 0:
         raise MxqError("invalid sizes for moe_plan")
     return b
@@ -397,17 +411,15 @@ def moe_plan(ids: torch.Tensor, offs: torch.Tensor, rows: torch.Tensor, src: tor
     """ids int32 (any shape, n slots); offs int32 (E,) receives the experts' end offsets,
     rows int32 (n) the row of each slot, src int32 (n) the slot of each row; workspace
     uint8 of moe_plan_workspace_bytes(n, E) (None where that is 0)."""
-    a = _Args()
-    pi = a(ids, torch.int32, "ids")
-    n = ids.numel()
-    po = a(offs, torch.int32, "offs")
-    pr = a(rows, torch.int32, "rows", n)
-    ps = a(src, torch.int32, "src", n)
-    pw = a.optional(workspace, torch.uint8, "workspace")
-    E = offs.numel()
-    if (0 if workspace is None else workspace.numel()) < moe_plan_workspace_bytes(n, E):
+    dev = _first(ids, "ids")
+    n, E = ids.numel(), offs.numel()
+    size = 0 if workspace is None else workspace.numel()
+    if size < moe_plan_workspace_bytes(n, E):
         raise MxqError("workspace is smaller than moe_plan_workspace_bytes")
-    a.run(lib().moe_plan, pi, n, E, po, pr, ps, pw, stream=stream)
+    i32 = torch.int32
+    _run(lib().moe_plan, dev, stream, _arg(ids, i32, "ids", n, dev), n, E, _arg(offs, i32, "offs", E, dev),
+         _arg(rows, i32, "rows", n, dev), _arg(src, i32, "src", n, dev),
+         _opt(workspace, torch.uint8, "workspace", size, dev))
 
 
 def rmsnorm_mx_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float, q: torch.Tensor, s: torch.Tensor,
@@ -417,22 +429,16 @@ def rmsnorm_mx_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float, q: to
     (M, D/32) receive the MXFP8 norm of x + residual; optional outputs: res_out bf16 (M, D)
     the sum (may be x or residual itself), y bf16 (M, D) the norm, rstd fp32 (M,)."""
     M, D = _two(x, "x", "(M, D)")
-    n = M * D
-    a = _Args()
-    bf = torch.bfloat16
-    px = a(x, bf, "x")
-    pw, ty = a.typed(weight, "weight", D)
-    pq = a(q, torch.uint8, "q", n)
-    ps = a(s, torch.uint8, "s", n // 32)
-    pr = a.optional(residual, bf, "residual", n)
-    po = a.optional(res_out, bf, "res_out", n)
-    py = a.optional(y, bf, "y", n)
-    pt = a.optional(rstd, torch.float32, "rstd", M)
-    a.run(lib().rmsnorm_mx_quantize, px, pr, pw, ty, M, D, eps, po, py, pq, ps, pt, stream=stream)
+    dev, ty, n = _first(x, "x"), _type_of(weight, "weight"), M * D
+    bf, u8 = torch.bfloat16, torch.uint8
+    _run(lib().rmsnorm_mx_quantize, dev, stream, _arg(x, bf, "x", n, dev), _opt(residual, bf, "residual", n, dev),
+         _arg(weight, _DTYPES[ty], "weight", D, dev), ty, M, D, eps, _opt(res_out, bf, "res_out", n, dev),
+         _opt(y, bf, "y", n, dev), _arg(q, u8, "q", n, dev), _arg(s, u8, "s", n // 32, dev),
+         _opt(rstd, torch.float32, "rstd", M, dev))
 
 
 def rmsnorm_backward_workspace_bytes(M: int, D: int) -> int:
-    b = int(lib().rmsnorm_backward_workspace_bytes(M, D))
+    b = lib().rmsnorm_backward_workspace_bytes(M, D)
     if b < 0:
         raise MxqError("invalid sizes for rmsnorm_backward")
     return b
@@ -445,20 +451,15 @@ def rmsnorm_backward(grad_y: torch.Tensor, h: torch.Tensor, weight: torch.Tensor
     (M,); grad_x bf16 (M, D) and grad_weight fp32 (D,) receive the gradients; workspace
     uint8 of rmsnorm_backward_workspace_bytes(M, D)."""
     M, D = _two(grad_y, "grad_y", "(M, D)")
-    n = M * D
-    a = _Args()
-    bf = torch.bfloat16
-    pg = a(grad_y, bf, "grad_y")
-    ph = a(h, bf, "h", n)
-    pw, ty = a.typed(weight, "weight", D)
-    pr = a(rstd, torch.float32, "rstd", M)
-    pe = a.optional(grad_res, bf, "grad_res", n)
-    po = a(grad_x, bf, "grad_x", n)
-    pd = a(grad_weight, torch.float32, "grad_weight", D)
-    ws = a(workspace, torch.uint8, "workspace")
-    if workspace.numel() < rmsnorm_backward_workspace_bytes(M, D):
+    dev, ty, n = _first(grad_y, "grad_y"), _type_of(weight, "weight"), M * D
+    bf, f32 = torch.bfloat16, torch.float32
+    size = workspace.numel()
+    if size < rmsnorm_backward_workspace_bytes(M, D):
         raise MxqError("workspace is smaller than rmsnorm_backward_workspace_bytes")
-    a.run(lib().rmsnorm_backward, pg, ph, pw, ty, pr, pe, M, D, po, pd, ws, stream=stream)
+    _run(lib().rmsnorm_backward, dev, stream, _arg(grad_y, bf, "grad_y", n, dev), _arg(h, bf, "h", n, dev),
+         _arg(weight, _DTYPES[ty], "weight", D, dev), ty, _arg(rstd, f32, "rstd", M, dev),
+         _opt(grad_res, bf, "grad_res", n, dev), M, D, _arg(grad_x, bf, "grad_x", n, dev),
+         _arg(grad_weight, f32, "grad_weight", D, dev), _arg(workspace, torch.uint8, "workspace", size, dev))
 
 
 def mxfp4_quantize(x: torch.Tensor, q: torch.Tensor, s: torch.Tensor | None = None,
@@ -468,33 +469,29 @@ def mxfp4_quantize(x: torch.Tensor, q: torch.Tensor, s: torch.Tensor | None = No
     sf_blocked uint8 (mx_scales_blocked_bytes), or both; with offs (int32 end offsets) the
     tiles are laid out per group, and rows in no group are left out."""
     batch, rows, cols = _bsc(x)
-    n = batch * rows * cols
-    a = _Args()
-    px = a(x, torch.bfloat16, "x")
-    pq = a(q, torch.uint8, "q", n // 2)
-    ps = a.optional(s, torch.uint8, "s", n // 32)
-    pf = a.optional(sf_blocked, torch.uint8, "sf_blocked")
-    po = a.optional(offs, torch.int32, "offs")
+    dev, n, u8 = _first(x, "x"), batch * rows * cols, torch.uint8
     G = 0 if offs is None else offs.numel()
-    if s is None and sf_blocked is None:
+    size = 0
+    if sf_blocked is not None:
+        size = sf_blocked.numel()
+        if size < mx_scales_blocked_bytes(batch, rows, cols // 32, G):
+            raise MxqError("sf_blocked is smaller than mx_scales_blocked_bytes")
+    elif s is None:
         raise MxqError("mxfp4_quantize needs s or sf_blocked for the scales")
     if offs is not None and (sf_blocked is None or G == 0):
         raise MxqError("offs needs sf_blocked and at least one group")
-    if sf_blocked is not None and sf_blocked.numel() < mx_scales_blocked_bytes(batch, rows, cols // 32, G):
-        raise MxqError("sf_blocked is smaller than mx_scales_blocked_bytes")
-    a.run(lib().mxfp4_quantize, px, batch, rows, cols, pq, ps, pf, po, G, stream=stream)
+    _run(lib().mxfp4_quantize, dev, stream, _arg(x, torch.bfloat16, "x", n, dev), batch, rows, cols,
+         _arg(q, u8, "q", n // 2, dev), _opt(s, u8, "s", n // 32, dev), _opt(sf_blocked, u8, "sf_blocked", size, dev),
+         _opt(offs, torch.int32, "offs", G, dev), G)
 
 
 def mxfp4_dequantize(q: torch.Tensor, s: torch.Tensor, y: torch.Tensor, stream=None) -> None:
     """q uint8 (.., cols/2) and s uint8 (.., cols/32) from mxfp4_quantize -> y bf16
     (rows, cols) or (batch, rows, cols)."""
     batch, rows, cols = _bsc(y)
-    n = batch * rows * cols
-    a = _Args()
-    pq = a(q, torch.uint8, "q", n // 2)
-    ps = a(s, torch.uint8, "s", n // 32)
-    py = a(y, torch.bfloat16, "y")
-    a.run(lib().mxfp4_dequantize, pq, ps, batch * rows, cols, py, stream=stream)
+    dev, n = _first(y, "y"), batch * rows * cols
+    _run(lib().mxfp4_dequantize, dev, stream, _arg(q, torch.uint8, "q", n // 2, dev),
+         _arg(s, torch.uint8, "s", n // 32, dev), batch * rows, cols, _arg(y, torch.bfloat16, "y", n, dev))
 
 
 def mxfp4_grouped_gemm(qa: torch.Tensor, sfa_blocked: torch.Tensor, qb: torch.Tensor, sfb_blocked: torch.Tensor,
@@ -508,16 +505,13 @@ def mxfp4_grouped_gemm(qa: torch.Tensor, sfa_blocked: torch.Tensor, qb: torch.Te
     G, N, Kb2 = qb.shape
     if Kb2 != Kb or offs.numel() != G:
         raise MxqError("qa, qb and offs disagree on K or G")
-    K = 2 * Kb
-    a = _Args()
-    pa = a(qa, torch.uint8, "qa")
-    pb = a(qb, torch.uint8, "qb")
-    psa = a(sfa_blocked, torch.uint8, "sfa_blocked")
-    psb = a(sfb_blocked, torch.uint8, "sfb_blocked")
-    if sfa_blocked.numel() < mx_scales_blocked_bytes(1, M, K // 32, G):
+    K, dev, u8 = 2 * Kb, _first(qa, "qa"), torch.uint8
+    na, nb = sfa_blocked.numel(), sfb_blocked.numel()
+    if na < mx_scales_blocked_bytes(1, M, K // 32, G):
         raise MxqError("sfa_blocked is smaller than mx_scales_blocked_bytes(1, M, K/32, G)")
-    if sfb_blocked.numel() < mx_scales_blocked_bytes(G, N, K // 32, 0):
+    if nb < mx_scales_blocked_bytes(G, N, K // 32, 0):
         raise MxqError("sfb_blocked is smaller than mx_scales_blocked_bytes(G, N, K/32, 0)")
-    po = a(offs, torch.int32, "offs")
-    pout = a(out, torch.bfloat16, "out", M * N)
-    a.run(lib().mxfp4_grouped_gemm, pa, psa, pb, psb, po, G, M, N, K, pout, stream=stream)
+    _run(lib().mxfp4_grouped_gemm, dev, stream, _arg(qa, u8, "qa", M * Kb, dev),
+         _arg(sfa_blocked, u8, "sfa_blocked", na, dev), _arg(qb, u8, "qb", G * N * Kb, dev),
+         _arg(sfb_blocked, u8, "sfb_blocked", nb, dev), _arg(offs, torch.int32, "offs", G, dev), G, M, N, K,
+         _arg(out, torch.bfloat16, "out", M * N, dev))
