@@ -13,8 +13,10 @@
 // repeated.  With scores spread as a router's are, that happens in well under one row of
 // a hundred, so the 64-bit pass costs nothing on average.
 //
-// One warp per row, lane l holding the elements l, l + 32, ...; nothing is bound by
-// arithmetic throughput, see the launcher for what was measured.
+// One warp per row.  Lane l holds the NI consecutive elements l NI .. l NI + NI - 1 (NI the
+// power of two that covers E), so that the lowest index of equal candidates is the lowest
+// lane's, a group is a run of lanes, and a row loads in 16-byte pieces.  Bound by
+// instruction issue: a row of 256 in 8 groups takes about 600 warp instructions.
 
 #include <algorithm>
 #include <type_traits>
@@ -119,43 +121,33 @@ __device__ __forceinline__ void scores(const float (&l)[NI], int score, R (&p)[N
     for (int i = 0; i < NI; ++i) p[i] *= inv;
 }
 
-// How far the 32-bit value of a candidate c = p + b may be from the exact one: the score's
-// relative error (l - max rounded: |l - max| 2^-24 <= 104 * 2^-24 before the score is zero
-// in 32 bits; exp within 2 units in the last place; the sum of up to 1024 terms in chains
-// of 32 + 5 additions; two roundings more: together under 2^-16), the addition's rounding,
-// and the underflow of scores below 2^-126.
-constexpr float RT_REL = 0x1p-16f;
-__device__ __forceinline__ float cand_err(float p, float c) {
-    return p * RT_REL + fabsf(c) * 0x1p-23f + 0x1p-126f;
+// How far the 32-bit value of a candidate c = p + b may be from the exact one.  Relative
+// error of a softmax score: l - max rounded (|l - max| 2^-24 <= 104 * 2^-24 before the score
+// is zero in 32 bits), exp within 2 units in the last place, the sum of up to 1024 terms in
+// chains of 32 + 5 additions, two roundings more: together under 2^-16.  Of a sigmoid:
+// the argument is exact; exp, one addition, a reciprocal and a product: under 2^-20.  Then
+// the addition's rounding, and the underflow of scores below 2^-126.
+constexpr float RT_REL = 0x1p-16f, RT_REL_SIGMOID = 0x1p-20f;
+__device__ __forceinline__ float cand_err(float rel, float p, float c) {
+    // p comes as c - b, itself rounded
+    return p * rel + fabsf(c) * 0x1p-22f + 0x1p-126f;
 }
 
-// The choice, in type R.  On return lane j < k holds the id of the j-th choice in `id` (-1
-// if there are fewer candidates).  Returns false (float only) if the order is in doubt.
-// `sc` is the warp's shared row of E values of type R.
-template <int NI, typename R>
-__device__ __forceinline__ bool choose(const float (&l)[NI], const RouteArgs& a, R* sc, int lane, int& id) {
-    const R NEG = neg_inf<R>();
+// The choice in 64 bits: lane j < k gets the id of the j-th (-1 if there are fewer).  The
+// lane holds the elements lane + 32 i; `sc` is the warp's shared row of E values.
+template <int NI>
+__device__ __forceinline__ void choose_in_64(const float (&l)[NI], const RouteArgs& a, double* sc, int lane, int& id) {
+    const double NEG = neg_inf<double>();
     const bool have_bias = a.bias != nullptr;
-    const bool need_p = have_bias || (a.n_groups > 1 && a.group_top == 2);
-    R c[NI];
-    R p[NI];
-    if (need_p) scores<NI, R>(l, a.score, p);
-    bool sure = true;
+    const bool by_p = a.n_groups > 1 && !have_bias && a.group_top == 2;
+    double c[NI], p[NI];
+    scores<NI, double>(l, a.score, p);
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
         const int e = lane + 32 * i;
-        if (!need_p) p[i] = (R)0;
-        if (l[i] == neg_inf<float>())
-            c[i] = NEG;
-        else if (have_bias)
-            c[i] = p[i] + (R)__ldg(a.bias + e);
-        else
-            c[i] = (R)l[i];
+        c[i] = l[i] == neg_inf<float>() ? NEG : have_bias ? p[i] + (double)__ldg(a.bias + e) : (double)l[i];
     }
     if (a.n_groups > 1) {
-        // the value that groups are ranked by: the candidate, or the score where the sum of
-        // two is wanted and the candidates are logits
-        const bool by_p = !have_bias && a.group_top == 2;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
             const int e = lane + 32 * i;
@@ -163,13 +155,10 @@ __device__ __forceinline__ bool choose(const float (&l)[NI], const RouteArgs& a,
         }
         __syncwarp();
         const int gs = a.E / a.n_groups;
-        R best = NEG, second = NEG;
-        if (lane < a.n_groups) {
+        double best = NEG, second = NEG;
+        if (lane < a.n_groups)
             for (int j = 0; j < gs; ++j) {
-                // start at the lane's own number so that the lanes meet in different banks
-                int jj = j + lane;
-                if (jj >= gs) jj -= gs * (jj / gs);
-                const R v = sc[lane * gs + jj];
+                const double v = sc[lane * gs + j];
                 if (v > best) {
                     second = best;
                     best = v;
@@ -177,46 +166,25 @@ __device__ __forceinline__ bool choose(const float (&l)[NI], const RouteArgs& a,
                     second = v;
                 }
             }
-        }
         __syncwarp();
         const bool some = best > NEG;
-        R gsum = best;
+        double gsum = best;
         if (a.group_top == 2 && some && second > NEG) gsum = best + second;
         int before = 0;
         for (int h = 0; h < a.n_groups; ++h) {
-            const R o = __shfl_sync(FULL_MASK, gsum, h);
+            const double o = __shfl_sync(FULL_MASK, gsum, h);
             if (o > gsum || (o == gsum && h < lane)) ++before;
         }
-        const bool kept = lane < a.n_groups && some && before < a.top_groups;
-        const unsigned kept_mask = __ballot_sync(FULL_MASK, kept);
-        if (sizeof(R) == 4 && need_p) {
-            // the border: the worst kept group against the best one left out
-            float lo = warp_max(kept ? -(float)gsum : neg_inf<float>());
-            float hi = warp_max(lane < a.n_groups && some && !kept ? (float)gsum : neg_inf<float>());
-            // each group's sum has at most two candidates' errors and one addition's; with a
-            // bias the scores are bounded by 1 and the roundings by the candidates' magnitudes
-            const float mag = warp_max(some ? fabsf((float)best) + (second > NEG ? fabsf((float)second) : 0.0f) : 0.0f);
-            if (hi > neg_inf<float>() && lo > neg_inf<float>()) {
-                lo = -lo;
-                const float err = by_p ? (lo + hi) * (2.0f * RT_REL) + 0x1p-120f : 4.0f * RT_REL + mag * 0x1p-21f;
-                if (!(lo - hi > err)) sure = false;
-            }
-        }
+        const unsigned kept = __ballot_sync(FULL_MASK, lane < a.n_groups && some && before < a.top_groups);
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
             const int e = lane + 32 * i;
-            const int g = e < a.E ? e / gs : 0;
-            if (!((kept_mask >> g) & 1u)) c[i] = NEG;
+            if (!((kept >> (e < a.E ? e / gs : 0)) & 1u)) c[i] = NEG;
         }
     }
-    // k extractions (one more where the order may be in doubt); a lane keeps its own best
     id = -1;
-    const bool check = sizeof(R) == 4 && have_bias;
-    const int n = check ? a.k + 1 : a.k;
-    R prev = NEG;
-    float prev_l = 0.0f, prev_b = 0.0f, prev_err = 0.0f;
-    for (int j = 0; j < n; ++j) {
-        R v = NEG;
+    for (int j = 0; j < a.k; ++j) {
+        double v = NEG;
         int at = 0x7FFFFFFF;
 #pragma unroll
         for (int i = 0; i < NI; ++i)
@@ -226,31 +194,136 @@ __device__ __forceinline__ bool choose(const float (&l)[NI], const RouteArgs& a,
             }
         warp_argmax(v, at);
         if (!(v > NEG)) break;
-        if (j < a.k && lane == j) id = at;
-        float wl = 0.0f, wp = 0.0f;
+        if (lane == j) id = at;
 #pragma unroll
         for (int i = 0; i < NI; ++i)
-            if (at == lane + 32 * i) {
-                c[i] = NEG;
-                wl = l[i];
-                wp = (float)p[i];
+            if (at == lane + 32 * i) c[i] = NEG;
+    }
+}
+
+// ---- 32-bit choice -------------------------------------------------------------------------------
+
+__device__ __forceinline__ float redux_max(float v) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xFFFFFFFF;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+__device__ __forceinline__ float widen(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
+__device__ __forceinline__ float widen(float v) { return v; }
+
+// The lane's elements as fp32, -inf past the row.  `vec`: rows and lanes start on the
+// boundaries that the widest load wants.
+template <int NI, typename L>
+__device__ __forceinline__ void load_row(const L* __restrict__ row, int E, bool vec, int lane, float (&l)[NI]) {
+    constexpr int BYTES = NI * (int)sizeof(L) < 16 ? NI * (int)sizeof(L) : 16;
+    constexpr int PER = BYTES / (int)sizeof(L);  // elements per piece
+    const int e0 = lane * NI;
+    if (vec && PER > 1) {
+#pragma unroll
+        for (int i = 0; i < NI; i += PER) {
+            L v[PER];
+            if (e0 + i < E) {
+                if (BYTES == 16)
+                    *reinterpret_cast<uint4*>(v) = ld_nc_v4(row + e0 + i);
+                else if (BYTES == 8)
+                    *reinterpret_cast<uint2*>(v) = ld_nc_v2(row + e0 + i);
+                else
+                    *reinterpret_cast<uint32_t*>(v) = __ldg(reinterpret_cast<const uint32_t*>(row + e0 + i));
             }
-        if (check) {
-            wl = __shfl_sync(FULL_MASK, wl, at & 31);
-            wp = __shfl_sync(FULL_MASK, wp, at & 31);
-            const float wb = __ldg(a.bias + at);
-            const float err = cand_err(wp, (float)v);
-            // infinite candidates (an infinite bias) tie by index, exactly
-            if (j > 0 && !((float)(prev - v) > prev_err + err) && !(wl == prev_l && wb == prev_b) &&
-                fabsf((float)v) < __int_as_float(0x7F800000))
-                sure = false;
-            prev = v;
-            prev_l = wl;
-            prev_b = wb;
-            prev_err = err;
+#pragma unroll
+            for (int j = 0; j < PER; ++j) l[i + j] = e0 + i < E ? widen(v[j]) : neg_inf<float>();
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) l[i] = e0 + i < E ? ld_logit(row + e0 + i) : neg_inf<float>();
+    }
+}
+
+// Whether load_row may use its pieces: every row starts on a piece's boundary.
+template <int NI, typename L>
+__host__ __device__ constexpr bool row_vec(int E) {
+    return E % (NI * (int)sizeof(L) < 16 ? NI : 16 / (int)sizeof(L)) == 0;
+}
+
+// Descending order within the lane, equal values by index: neighbours are exchanged only
+// where the later one is larger.
+template <int NI>
+__device__ __forceinline__ void sort_lane(float (&c)[NI], int (&x)[NI]) {
+#pragma unroll
+    for (int n = 1; n < NI; ++n)
+#pragma unroll
+        for (int i = n; i > 0; --i) {
+            const bool up = c[i] > c[i - 1];
+            const float hi = up ? c[i] : c[i - 1], lo = up ? c[i - 1] : c[i];
+            const int xh = up ? x[i] : x[i - 1], xl = up ? x[i - 1] : x[i];
+            c[i - 1] = hi, c[i] = lo, x[i - 1] = xh, x[i] = xl;
+        }
+}
+
+// The row's n best candidates in order, equal ones by index: lane j < 32 gets the j-th
+// (id -1 if there is none); the last one asked for also goes to every lane.  Destroys c.
+template <int NI>
+__device__ __forceinline__ void extract(float (&c)[NI], int n, int lane, int& id, float& val, int& last_id,
+                                        float& last_val) {
+    constexpr bool SORTED = NI <= 8;  // above, a sort costs more than looking again
+    int x[NI];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) x[i] = lane * NI + i;
+    if (SORTED) sort_lane<NI>(c, x);
+    id = -1;
+    val = neg_inf<float>();
+    for (int j = 0; j < n; ++j) {
+        float head = c[0];
+        int at = x[0];
+        if (!SORTED) {
+#pragma unroll
+            for (int i = 1; i < NI; ++i)
+                if (c[i] > head) {
+                    head = c[i];
+                    at = x[i];
+                }
+        }
+        const float m = redux_max(head);
+        const unsigned who = __ballot_sync(FULL_MASK, head == m);
+        const int win = __ffs(who) - 1;
+        const int e = m > neg_inf<float>() ? __shfl_sync(FULL_MASK, at, win) : -1;
+        if (lane == j) {
+            id = e;
+            val = m;
+        }
+        last_id = e;
+        last_val = m;
+        if (e < 0) break;  // nothing is left: the same for the ones not asked
+        if (lane == win) {
+            if (SORTED) {
+#pragma unroll
+                for (int i = 0; i + 1 < NI; ++i) {
+                    c[i] = c[i + 1];
+                    x[i] = x[i + 1];
+                }
+                c[NI - 1] = neg_inf<float>();
+            } else {
+#pragma unroll
+                for (int i = 0; i < NI; ++i)
+                    if (x[i] == e) c[i] = neg_inf<float>();
+            }
         }
     }
-    return sizeof(R) == 8 || sure;
+}
+
+// The exact choice of one row (rare).
+template <int NI, typename L>
+__device__ __noinline__ int choose_exact(const L* row, RouteArgs a, double* sc, int lane) {
+    float l[NI];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+        const int e = lane + 32 * i;
+        l[i] = e < a.E ? ld_logit(row + e) + 0.0f : neg_inf<float>();
+    }
+    int id;
+    choose_in_64<NI>(l, a, sc, lane, id);
+    return id;
 }
 
 template <int NI, typename L>
@@ -258,37 +331,178 @@ __global__ void __launch_bounds__(32 * RT_WARPS) moe_route_kernel(const L* __res
                                                                   float* __restrict__ weights,
                                                                   int32_t* __restrict__ ids) {
     extern __shared__ double route_rows[];
+    const float NEG = neg_inf<float>(), INF = __int_as_float(0x7F800000);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    double* row_s = route_rows + (int64_t)warp * a.E;
     const int64_t n_warps = (int64_t)gridDim.x * RT_WARPS;
+    const bool vec = row_vec<NI, L>(a.E);
+    const bool have_bias = a.bias != nullptr, grouped = a.n_groups > 1;
+    const bool by_p = grouped && !have_bias && a.group_top == 2;  // groups by scores, candidates logits
+    const bool need_p = have_bias || by_p;
+    const int gs = a.E / a.n_groups, gl = gs / NI;  // elements and lanes of a group
+    const bool runs = gl > 0 && gl * NI == gs && (gl & (gl - 1)) == 0;
+    float* row_s = reinterpret_cast<float*>(route_rows + (int64_t)warp * a.E);
     for (int64_t t = (int64_t)blockIdx.x * RT_WARPS + warp; t < a.T; t += n_warps) {
         const L* row = logits + t * a.E;
-        float l[NI];
-        bool bad = false;
+        float l[NI], c[NI];
+        load_row<NI, L>(row, a.E, vec, lane, l);
+        float top = NEG, sum = 0.0f;
+        uint32_t nan = 0;  // the largest magnitude's bits, doubled: above 0xFF000000 for a NaN
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-            const int e = lane + 32 * i;
-            l[i] = neg_inf<float>();
-            if (e < a.E) {
-                l[i] = ld_logit(row + e) + 0.0f;  // -0 becomes +0: the two are equal
-                // a NaN, or what makes one of a candidate, spoils the row
-                bad |= isnan(l[i]) || (a.score == 0 && l[i] == __int_as_float(0x7F800000));
-                if (a.bias) bad |= isnan(__ldg(a.bias + e)) && l[i] != neg_inf<float>();
+            nan = max(nan, __float_as_uint(l[i]) << 1);
+            top = fmaxf(top, l[i]);
+            l[i] += 0.0f;  // -0 becomes +0: the two are equal
+            c[i] = l[i];
+        }
+        const bool softmax_sum = a.score == 0 && (need_p || !a.renorm);
+        if (a.score == 0) top = redux_max(top);
+        if (need_p || softmax_sum) {
+            float p[NI];
+            if (a.score == 1) {
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
+                    const float u = expf(-fabsf(l[i])), inv = __frcp_rn(1.0f + u);
+                    p[i] = l[i] < 0.0f ? u * inv : inv;  // 0 for -inf
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
+                    p[i] = l[i] == NEG ? 0.0f : expf(l[i] - top);
+                    sum += p[i];
+                }
+                sum = warp_sum(sum);
+                if (need_p) {
+                    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+#pragma unroll
+                    for (int i = 0; i < NI; ++i) p[i] *= inv;
+                }
+            }
+            if (need_p) {
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
+                    if (have_bias) {
+                        const int e = lane * NI + i;
+                        c[i] = p[i] + (e < a.E ? __ldg(a.bias + e) : 0.0f);
+                        if (l[i] == NEG) c[i] = NEG;
+                        nan = max(nan, __float_as_uint(c[i]) << 1);
+                    } else if (l[i] != NEG) {
+                        c[i] = p[i];  // for the groups; the logits come back below
+                    }
+                }
             }
         }
-        if (__any_sync(FULL_MASK, bad)) {
+        if (__any_sync(FULL_MASK, nan > 0xFF000000u) || (a.score == 0 && top == INF)) {
             if (lane < a.k) {
                 weights[t * a.k + lane] = __int_as_float(0x7FC00000);
                 ids[t * a.k + lane] = lane;
             }
             continue;
         }
-        int id;
-        if (!choose<NI, float>(l, a, reinterpret_cast<float*>(row_s), lane, id))
-            choose<NI, double>(l, a, row_s, lane, id);
+        bool sure = true;
+        if (grouped) {
+            float best = NEG, second = NEG;
+            bool kept;
+            int g0;  // the lane's group (the first one where a lane holds several)
+            if (runs) {
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
+                    second = fmaxf(second, fminf(best, c[i]));
+                    best = fmaxf(best, c[i]);
+                }
+                for (int sh = 1; sh < gl; sh <<= 1) {
+                    const float ob = __shfl_xor_sync(FULL_MASK, best, sh), os = __shfl_xor_sync(FULL_MASK, second, sh);
+                    second = fmaxf(fmaxf(second, os), fminf(best, ob));
+                    best = fmaxf(best, ob);
+                }
+                g0 = lane / gl;
+            } else {
+                // any other shape: lane g scans group g in shared memory
+#pragma unroll
+                for (int i = 0; i < NI; ++i)
+                    if (lane * NI + i < a.E) row_s[lane * NI + i] = c[i];
+                __syncwarp();
+                if (lane < a.n_groups)
+                    for (int j = 0; j < gs; ++j) {
+                        const float v = row_s[lane * gs + j];
+                        second = fmaxf(second, fminf(best, v));
+                        best = fmaxf(best, v);
+                    }
+                __syncwarp();
+                g0 = lane;
+            }
+            const int step = runs ? gl : 1;  // lane of group g: g * step
+            const bool in = g0 < a.n_groups;
+            const bool some = in && best > NEG;
+            float gsum = best;
+            if (a.group_top == 2 && some && second > NEG) gsum = best + second;
+            int before = 0;
+            for (int h = 0; h < a.n_groups; ++h) {
+                const float o = __shfl_sync(FULL_MASK, gsum, h * step);
+                if (o > gsum || (o == gsum && h < g0)) ++before;
+            }
+            kept = some && before < a.top_groups;
+            if (need_p) {
+                // the border: the worst kept group against the best one left out.  Each sum has
+                // at most two candidates' errors and one addition's; with a bias the scores are
+                // bounded by 1 and the roundings by the candidates' magnitudes
+                const float lo = -redux_max(kept ? -gsum : NEG);
+                const float hi = redux_max(some && !kept ? gsum : NEG);
+                if (hi > NEG && lo < INF) {
+                    const float rel = a.score == 1 ? RT_REL_SIGMOID : RT_REL;
+                    float err = (lo + hi) * (2.0f * rel) + 0x1p-120f;
+                    if (!by_p) {
+                        const float mag =
+                            redux_max(some ? fabsf(best) + (second > NEG ? fabsf(second) : 0.0f) : 0.0f);
+                        err = 4.0f * rel + mag * 0x1p-21f;
+                    }
+                    sure = lo - hi > err;
+                } else if (hi > NEG) {
+                    sure = false;  // infinite sums on both sides
+                }
+            }
+            if (runs) {
+#pragma unroll
+                for (int i = 0; i < NI; ++i) c[i] = !kept ? NEG : by_p ? l[i] : c[i];
+            } else {
+                const unsigned mask = __ballot_sync(FULL_MASK, kept);
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
+                    const int e = lane * NI + i;
+                    if (by_p) c[i] = l[i];
+                    if (e >= a.E || !((mask >> (e / gs)) & 1u)) c[i] = NEG;
+                }
+            }
+        }
+        // the k best; with a bias one more, to see that the order is beyond doubt
+        int id = -1, last_id = -1;
+        float val = NEG, last_val = NEG;
+        if (sure) {
+            extract<NI>(c, have_bias ? a.k + 1 : a.k, lane, id, val, last_id, last_val);
+            if (lane >= a.k) id = -1;
+            if (have_bias) {
+                // each against the next one: lane j has the j-th, every lane the last
+                const float lj = id >= 0 ? ld_logit(row + id) + 0.0f : 0.0f, bj = id >= 0 ? __ldg(a.bias + id) : 0.0f;
+                const float rel = a.score == 1 ? RT_REL_SIGMOID : RT_REL;
+                const float err = cand_err(rel, fabsf(val - bj), val);
+                int nid = __shfl_down_sync(FULL_MASK, id, 1);
+                float nv = __shfl_down_sync(FULL_MASK, val, 1), nl = __shfl_down_sync(FULL_MASK, lj, 1),
+                      nb = __shfl_down_sync(FULL_MASK, bj, 1), ne = __shfl_down_sync(FULL_MASK, err, 1);
+                if (lane == a.k - 1) {
+                    nid = last_id;
+                    nv = last_val;
+                    nl = nid >= 0 ? ld_logit(row + nid) + 0.0f : 0.0f;
+                    nb = nid >= 0 ? __ldg(a.bias + nid) : 0.0f;
+                    ne = cand_err(rel, fabsf(nv - nb), nv);
+                }
+                const bool close = id >= 0 && nid >= 0 && !(val - nv > err + ne) && !(lj == nl && bj == nb) &&
+                                   fabsf(val) < INF;  // infinite candidates tie by index, exactly
+                sure = !__any_sync(FULL_MASK, close);
+            }
+        }
+        if (!sure) id = choose_exact<NI, L>(row, a, route_rows + (int64_t)warp * a.E, lane);
         // ---- weights: lane j < k has the j-th choice
         const bool mine = lane < a.k && id >= 0;
-        const float lj = mine ? ld_logit(row + id) + 0.0f : neg_inf<float>();
+        const float lj = mine ? ld_logit(row + id) + 0.0f : NEG;
         float w = 0.0f;
         if (a.score == 1) {
             float q;
@@ -296,23 +510,16 @@ __global__ void __launch_bounds__(32 * RT_WARPS) moe_route_kernel(const L* __res
             if (!mine) w = 0.0f;
             if (a.renorm) w = w / (warp_sum(w) + 1e-20f);
         } else if (a.renorm) {
-            const float m = warp_max(lj);
+            const float m = redux_max(lj);
             w = mine ? expf(lj - m) : 0.0f;
             const float s = warp_sum(w);
             w = mine ? w / s : 0.0f;
         } else {
-            float m = neg_inf<float>(), s = 0.0f;
-#pragma unroll
-            for (int i = 0; i < NI; ++i) m = fmaxf(m, l[i]);
-            m = warp_max(m);
-#pragma unroll
-            for (int i = 0; i < NI; ++i) s += l[i] == neg_inf<float>() ? 0.0f : expf(l[i] - m);
-            s = warp_sum(s);
-            w = mine ? expf(lj - m) / s : 0.0f;
+            w = mine ? expf(lj - top) / sum : 0.0f;
         }
         if (lane < a.k) {
             weights[t * a.k + lane] = w * a.scale;
-            ids[t * a.k + lane] = id;
+            ids[t * a.k + lane] = mine ? id : -1;
         }
     }
 }
@@ -326,97 +533,133 @@ __global__ void __launch_bounds__(32 * RT_WARPS) moe_route_kernel(const L* __res
 //   sigmoid, renorm     r_j = p_j / (sum p + 1e-20): dl_j = s r_j (1 - p_j) (g_j - sum_m g_m r_m)
 // and 0 for every other expert.  A warp per row builds the row in shared memory (scattered
 // entries) and writes it out in order.
-template <typename L>
-__device__ __forceinline__ void st_grad(L* p, float v);
-template <>
-__device__ __forceinline__ void st_grad<float>(float* p, float v) { *p = v; }
-template <>
-__device__ __forceinline__ void st_grad<uint16_t>(uint16_t* p, float v) { *p = (uint16_t)cvt_bf16x2(v, 0.0f); }
+// The lane's NI consecutive values to the row, in the pieces of load_row.
+template <int NI>
+__device__ __forceinline__ void store_row(float* row, int E, bool vec, int lane, const float (&v)[NI]) {
+    const int e0 = lane * NI;
+    if (vec && NI >= 2) {
+        constexpr int PER = NI < 4 ? 2 : 4;
+#pragma unroll
+        for (int i = 0; i < NI; i += PER)
+            if (e0 + i < E) {
+                if (PER == 4)
+                    *reinterpret_cast<float4*>(row + e0 + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                else
+                    *reinterpret_cast<float2*>(row + e0 + i) = make_float2(v[i], v[i + 1]);
+            }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+            if (e0 + i < E) row[e0 + i] = v[i];
+    }
+}
+template <int NI>
+__device__ __forceinline__ void store_row(uint16_t* row, int E, bool vec, int lane, const float (&v)[NI]) {
+    const int e0 = lane * NI;
+    if (vec && NI >= 2) {
+        constexpr int PER = NI < 8 ? (NI < 2 ? 2 : NI) : 8;
+#pragma unroll
+        for (int i = 0; i < NI; i += PER)
+            if (e0 + i < E) {
+                uint32_t w[PER > 1 ? PER / 2 : 1];
+#pragma unroll
+                for (int j = 0; j < PER / 2; ++j) w[j] = cvt_bf16x2(v[i + 2 * j], v[i + 2 * j + 1]);
+                if (PER == 8)
+                    *reinterpret_cast<uint4*>(row + e0 + i) = *reinterpret_cast<uint4*>(w);
+                else if (PER == 4)
+                    *reinterpret_cast<uint2*>(row + e0 + i) = *reinterpret_cast<uint2*>(w);
+                else
+                    *reinterpret_cast<uint32_t*>(row + e0 + i) = w[0];
+            }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+            if (e0 + i < E) row[e0 + i] = (uint16_t)cvt_bf16x2(v[i], 0.0f);
+    }
+}
 
 template <int NI, typename L>
 __global__ void __launch_bounds__(32 * RT_WARPS) moe_route_backward_kernel(
     const L* __restrict__ logits, RouteArgs a, const int32_t* __restrict__ ids, const float* __restrict__ gw,
     L* __restrict__ gl) {
-    extern __shared__ float grad_rows[];
+    // a row per warp: the lanes' values lie with a stride of NI + 1, so that they meet in
+    // different banks
+    __shared__ float grad_rows[RT_WARPS][32 * (NI + 1)];
+    const float NEG = neg_inf<float>();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    float* row_s = grad_rows + (int64_t)warp * a.E;
+    float* row_s = grad_rows[warp];
+    const bool vec = row_vec<NI, L>(a.E);
     const int64_t n_warps = (int64_t)gridDim.x * RT_WARPS;
     for (int64_t t = (int64_t)blockIdx.x * RT_WARPS + warp; t < a.T; t += n_warps) {
         const L* row = logits + t * a.E;
         int id = -1;
         float g = 0.0f;
         if (lane < a.k) {
-            id = ids[t * a.k + lane];
+            id = __ldg(ids + t * a.k + lane);
             if (id < 0 || id >= a.E) id = -1;
-            if (id >= 0) g = gw[t * a.k + lane] * a.scale;
+            if (id >= 0) g = __ldg(gw + t * a.k + lane) * a.scale;
         }
         const bool mine = id >= 0;
-        const float lj = mine ? ld_logit(row + id) : neg_inf<float>();
-        float d = 0.0f, dot = 0.0f;
+        const float lj = mine ? ld_logit(row + id) : NEG;
+        float d = 0.0f;
         float base[NI];
+        if (a.score == 0 && !a.renorm) {
+            load_row<NI, L>(row, a.E, vec, lane, base);
+            float m = NEG, s = 0.0f;
 #pragma unroll
-        for (int i = 0; i < NI; ++i) base[i] = 0.0f;
-        if (a.score == 1) {
-            float p, q;
-            sigmoid_pair<float>(lj, p, q);
-            if (!mine) p = 0.0f;
-            if (a.renorm) {
-                const float r = p / (warp_sum(p) + 1e-20f);
-                d = r * q * (g - warp_sum(g * r));
-            } else {
-                d = g * p * q;
-            }
-        } else if (a.renorm) {
-            const float m = warp_max(lj);
-            const float ex = mine && lj > neg_inf<float>() ? expf(lj - m) : (lj == lj ? 0.0f : lj);
-            const float s = warp_sum(ex);
-            const float r = mine && s != 0.0f ? ex / s : 0.0f;
-            d = r * (g - warp_sum(g * r));
-        } else {
-            float m = neg_inf<float>(), s = 0.0f;
+            for (int i = 0; i < NI; ++i) m = fmaxf(m, base[i]);
+            m = redux_max(m);
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
-                const int e = lane + 32 * i;
-                base[i] = e < a.E ? ld_logit(row + e) : neg_inf<float>();
-                m = fmaxf(m, base[i]);
-            }
-            m = warp_max(m);
-#pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                base[i] = base[i] == neg_inf<float>() ? 0.0f : expf(base[i] - m);
+                base[i] = base[i] == NEG ? 0.0f : expf(base[i] - m);
                 s += base[i];
             }
             s = warp_sum(s);
             const float inv = s != 0.0f ? 1.0f / s : 0.0f;
-            const float p = mine && lj != neg_inf<float>() ? expf(lj - m) * inv : 0.0f;
+            const float p = mine && lj != NEG ? expf(lj - m) * inv : 0.0f;
             d = g * p;
-            dot = warp_sum(d);
+            const float f = -warp_sum(d) * inv;
 #pragma unroll
-            for (int i = 0; i < NI; ++i) base[i] *= -dot * inv;
+            for (int i = 0; i < NI; ++i) base[i] *= f;
+        } else {
+#pragma unroll
+            for (int i = 0; i < NI; ++i) base[i] = 0.0f;
+            if (a.score == 1) {
+                float p, q;
+                sigmoid_pair<float>(lj, p, q);
+                if (!mine) p = 0.0f;
+                if (a.renorm) {
+                    const float r = p / (warp_sum(p) + 1e-20f);
+                    d = r * q * (g - warp_sum(g * r));
+                } else {
+                    d = g * p * q;
+                }
+            } else {
+                const float m = warp_max(lj);
+                const float ex = mine && lj > NEG ? expf(lj - m) : (lj == lj ? 0.0f : lj);
+                const float s = warp_sum(ex);
+                const float r = mine && s != 0.0f ? ex / s : 0.0f;
+                d = r * (g - warp_sum(g * r));
+            }
         }
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            const int e = lane + 32 * i;
-            if (e < a.E) row_s[e] = base[i];
-        }
+        for (int i = 0; i < NI; ++i) row_s[lane * (NI + 1) + i] = base[i];
         __syncwarp();
         // the chosen entries; an index that comes twice is added in the order of its slots
+        const int at = mine ? id / NI * (NI + 1) + id % NI : 0;
         const unsigned same = __match_any_sync(FULL_MASK, mine ? id : -1 - lane);
         if (__any_sync(FULL_MASK, (same & (same - 1)) != 0)) {
             for (int j = 0; j < a.k; ++j) {
-                if (lane == j && mine) row_s[id] += d;
+                if (lane == j && mine) row_s[at] += d;
                 __syncwarp();
             }
         } else if (mine) {
-            row_s[id] += d;
+            row_s[at] += d;
         }
         __syncwarp();
-        L* out = gl + t * a.E;
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            const int e = lane + 32 * i;
-            if (e < a.E) st_grad<L>(out + e, row_s[e]);
-        }
+        for (int i = 0; i < NI; ++i) base[i] = row_s[lane * (NI + 1) + i];
+        store_row<NI>(gl + t * a.E, a.E, vec, lane, base);
         __syncwarp();
     }
 }
@@ -440,7 +683,7 @@ cudaError_t launch_moe_route(const void* logits, bool bf16, int64_t T, int E, co
     const RouteArgs a{bias, T, E, k, n_groups, top_groups, group_top, score, renorm ? 1 : 0, scale};
     const int64_t ctas = (T + RT_WARPS - 1) / RT_WARPS;
     const unsigned grid = (unsigned)std::min<int64_t>(ctas, (int64_t)sm_count() * 8);
-    const size_t smem = n_groups > 1 ? (size_t)RT_WARPS * E * sizeof(double) : 0;
+    const size_t smem = n_groups > 1 ? (size_t)RT_WARPS * E * sizeof(double) : 0;  // a row per warp, for the groups
     return by_width(E, [&](auto ni) {
         constexpr int NI = decltype(ni)::value;
         cudaError_t e = cudaSuccess;
@@ -469,14 +712,13 @@ cudaError_t launch_moe_route_backward(const void* logits, bool bf16, int64_t T, 
     const RouteArgs a{nullptr, T, E, k, 1, 1, 1, score, renorm ? 1 : 0, scale};
     const int64_t ctas = (T + RT_WARPS - 1) / RT_WARPS;
     const unsigned grid = (unsigned)std::min<int64_t>(ctas, (int64_t)sm_count() * 8);
-    const size_t smem = (size_t)RT_WARPS * E * sizeof(float);
     return by_width(E, [&](auto ni) {
         constexpr int NI = decltype(ni)::value;
         if (bf16)
-            moe_route_backward_kernel<NI, uint16_t><<<grid, 32 * RT_WARPS, smem, stream>>>(
+            moe_route_backward_kernel<NI, uint16_t><<<grid, 32 * RT_WARPS, 0, stream>>>(
                 static_cast<const uint16_t*>(logits), a, ids, grad_weights, static_cast<uint16_t*>(grad_logits));
         else
-            moe_route_backward_kernel<NI, float><<<grid, 32 * RT_WARPS, smem, stream>>>(
+            moe_route_backward_kernel<NI, float><<<grid, 32 * RT_WARPS, 0, stream>>>(
                 static_cast<const float*>(logits), a, ids, grad_weights, static_cast<float*>(grad_logits));
         return cudaGetLastError();
     });
