@@ -209,6 +209,25 @@ __device__ __forceinline__ float redux_max(float v) {
     return r;
 }
 
+// The same, NaN if any is.
+__device__ __forceinline__ float redux_max_nan(float v) {
+    float r;
+    asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xFFFFFFFF;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// 1 / v for 1 <= v <= 2, within one unit in the last place.
+__device__ __forceinline__ float rcp1(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
 __device__ __forceinline__ float widen(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
 __device__ __forceinline__ float widen(float v) { return v; }
 
@@ -312,6 +331,75 @@ __device__ __forceinline__ void extract(float (&c)[NI], int n, int lane, int& id
     }
 }
 
+// The same for n <= 16, by a threshold.  The n-th largest of the lanes' own maxima is at most
+// the row's n-th best candidate, so the candidates from it up are all that can be chosen:
+// about -32 ln(1 - n / 32) of them for values in no order (9 for n = 8, 22 for n = 16).  They
+// are gathered in index order, and each counts the ones before it.  False, with nothing
+// done, where more than 32 are left (rows of equal logits).
+struct Picked {
+    float val[33];
+    int id[33];
+};
+template <int NI>
+__device__ __forceinline__ bool select_few(const float (&c)[NI], int n, int lane, Picked* s, int& id, float& val,
+                                           int& last_id, float& last_val) {
+    const float NEG = neg_inf<float>();
+    float head = c[0];
+#pragma unroll
+    for (int i = 1; i < NI; ++i) head = fmaxf(head, c[i]);
+    float t = NEG, h = head;
+    for (int j = 0; j < n; ++j) {  // equal maxima leave together: the threshold only gets lower
+        t = redux_max(h);
+        if (h == t) h = NEG;
+    }
+    const float low = t > NEG ? t : -3.402823466e38f;  // fewer lanes than n have any: all finite ones
+    int mine = 0;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) mine += c[i] >= low;
+    int pos = mine;
+#pragma unroll
+    for (int sh = 1; sh < 32; sh <<= 1) {
+        const int o = __shfl_up_sync(FULL_MASK, pos, sh);
+        if (lane >= sh) pos += o;
+    }
+    const int cnt = __shfl_sync(FULL_MASK, pos, 31);
+    if (cnt > 32) return false;
+    pos -= mine;
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+        if (c[i] >= low) {
+            s->val[pos] = c[i];
+            s->id[pos++] = lane * NI + i;
+        }
+    __syncwarp();
+    float v = NEG;
+    int e = -1, rank = 0;
+    if (lane < cnt) {
+        v = s->val[lane];
+        e = s->id[lane];
+    }
+    for (int j = 0; j < cnt; ++j) {
+        const float o = __shfl_sync(FULL_MASK, v, j);
+        rank += o > v || (o == v && j < lane);
+    }
+    __syncwarp();
+    if (lane < cnt) {
+        s->val[rank] = v;
+        s->id[rank] = e;
+    }
+    __syncwarp();
+    id = -1;
+    val = NEG;
+    if (lane < min(cnt, n)) {
+        val = s->val[lane];
+        id = s->id[lane];
+    }
+    last_id = cnt >= n ? s->id[n - 1] : -1;
+    last_val = cnt >= n ? s->val[n - 1] : NEG;
+    __syncwarp();
+    return true;
+}
+
 // The exact choice of one row (rare).
 template <int NI, typename L>
 __device__ __noinline__ int choose_exact(const L* row, RouteArgs a, double* sc, int lane) {
@@ -327,10 +415,11 @@ __device__ __noinline__ int choose_exact(const L* row, RouteArgs a, double* sc, 
 }
 
 template <int NI, typename L>
-__global__ void __launch_bounds__(32 * RT_WARPS) moe_route_kernel(const L* __restrict__ logits, RouteArgs a,
+__global__ void __launch_bounds__(32 * RT_WARPS, NI <= 8 ? 4 : NI <= 16 ? 2 : 1) moe_route_kernel(const L* __restrict__ logits, RouteArgs a,
                                                                   float* __restrict__ weights,
                                                                   int32_t* __restrict__ ids) {
     extern __shared__ double route_rows[];
+    __shared__ Picked picked[RT_WARPS];
     const float NEG = neg_inf<float>(), INF = __int_as_float(0x7F800000);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t n_warps = (int64_t)gridDim.x * RT_WARPS;
@@ -341,27 +430,29 @@ __global__ void __launch_bounds__(32 * RT_WARPS) moe_route_kernel(const L* __res
     const int gs = a.E / a.n_groups, gl = gs / NI;  // elements and lanes of a group
     const bool runs = gl > 0 && gl * NI == gs && (gl & (gl - 1)) == 0;
     float* row_s = reinterpret_cast<float*>(route_rows + (int64_t)warp * a.E);
+    constexpr bool KEEP_BIAS = NI <= 8;  // the lane's biases stay in registers
+    float bias[KEEP_BIAS ? NI : 1];
+    if (KEEP_BIAS)
+#pragma unroll
+        for (int i = 0; i < NI; ++i) bias[i] = have_bias && lane * NI + i < a.E ? __ldg(a.bias + lane * NI + i) : 0.0f;
     for (int64_t t = (int64_t)blockIdx.x * RT_WARPS + warp; t < a.T; t += n_warps) {
         const L* row = logits + t * a.E;
         float l[NI], c[NI];
         load_row<NI, L>(row, a.E, vec, lane, l);
-        float top = NEG, sum = 0.0f;
-        uint32_t nan = 0;  // the largest magnitude's bits, doubled: above 0xFF000000 for a NaN
+        float top = l[0], sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-            nan = max(nan, __float_as_uint(l[i]) << 1);
-            top = fmaxf(top, l[i]);
-            l[i] += 0.0f;  // -0 becomes +0: the two are equal
+            top = max_nan(top, l[i]);
             c[i] = l[i];
         }
+        top = redux_max_nan(top);
         const bool softmax_sum = a.score == 0 && (need_p || !a.renorm);
-        if (a.score == 0) top = redux_max(top);
         if (need_p || softmax_sum) {
             float p[NI];
             if (a.score == 1) {
 #pragma unroll
                 for (int i = 0; i < NI; ++i) {
-                    const float u = expf(-fabsf(l[i])), inv = __frcp_rn(1.0f + u);
+                    const float u = expf(-fabsf(l[i])), inv = rcp1(1.0f + u);
                     p[i] = l[i] < 0.0f ? u * inv : inv;  // 0 for -inf
                 }
             } else {
@@ -377,21 +468,23 @@ __global__ void __launch_bounds__(32 * RT_WARPS) moe_route_kernel(const L* __res
                     for (int i = 0; i < NI; ++i) p[i] *= inv;
                 }
             }
-            if (need_p) {
+            if (have_bias) {
+                float worst = NEG;
 #pragma unroll
                 for (int i = 0; i < NI; ++i) {
-                    if (have_bias) {
-                        const int e = lane * NI + i;
-                        c[i] = p[i] + (e < a.E ? __ldg(a.bias + e) : 0.0f);
-                        if (l[i] == NEG) c[i] = NEG;
-                        nan = max(nan, __float_as_uint(c[i]) << 1);
-                    } else if (l[i] != NEG) {
-                        c[i] = p[i];  // for the groups; the logits come back below
-                    }
+                    const int e = lane * NI + i;
+                    const float b = KEEP_BIAS ? bias[KEEP_BIAS ? i : 0] : e < a.E ? __ldg(a.bias + e) : 0.0f;
+                    c[i] = l[i] == NEG ? NEG : p[i] + b;
+                    worst = max_nan(worst, c[i]);
                 }
+                if (__any_sync(FULL_MASK, isnan(worst))) top = worst = __int_as_float(0x7FC00000);
+            } else if (by_p) {
+#pragma unroll
+                for (int i = 0; i < NI; ++i)
+                    if (l[i] != NEG) c[i] = p[i];  // for the groups; the logits come back below
             }
         }
-        if (__any_sync(FULL_MASK, nan > 0xFF000000u) || (a.score == 0 && top == INF)) {
+        if (isnan(top) || (a.score == 0 && top == INF)) {
             if (lane < a.k) {
                 weights[t * a.k + lane] = __int_as_float(0x7FC00000);
                 ids[t * a.k + lane] = lane;
@@ -477,11 +570,13 @@ __global__ void __launch_bounds__(32 * RT_WARPS) moe_route_kernel(const L* __res
         int id = -1, last_id = -1;
         float val = NEG, last_val = NEG;
         if (sure) {
-            extract<NI>(c, have_bias ? a.k + 1 : a.k, lane, id, val, last_id, last_val);
+            const int n = have_bias ? a.k + 1 : a.k;
+            if (n > 16 || !select_few<NI>(c, n, lane, &picked[warp], id, val, last_id, last_val))
+                extract<NI>(c, n, lane, id, val, last_id, last_val);
             if (lane >= a.k) id = -1;
             if (have_bias) {
                 // each against the next one: lane j has the j-th, every lane the last
-                const float lj = id >= 0 ? ld_logit(row + id) + 0.0f : 0.0f, bj = id >= 0 ? __ldg(a.bias + id) : 0.0f;
+                const float lj = id >= 0 ? ld_logit(row + id) : 0.0f, bj = id >= 0 ? __ldg(a.bias + id) : 0.0f;
                 const float rel = a.score == 1 ? RT_REL_SIGMOID : RT_REL;
                 const float err = cand_err(rel, fabsf(val - bj), val);
                 int nid = __shfl_down_sync(FULL_MASK, id, 1);
@@ -490,7 +585,7 @@ __global__ void __launch_bounds__(32 * RT_WARPS) moe_route_kernel(const L* __res
                 if (lane == a.k - 1) {
                     nid = last_id;
                     nv = last_val;
-                    nl = nid >= 0 ? ld_logit(row + nid) + 0.0f : 0.0f;
+                    nl = nid >= 0 ? ld_logit(row + nid) : 0.0f;
                     nb = nid >= 0 ? __ldg(a.bias + nid) : 0.0f;
                     ne = cand_err(rel, fabsf(nv - nb), nv);
                 }
@@ -502,20 +597,19 @@ __global__ void __launch_bounds__(32 * RT_WARPS) moe_route_kernel(const L* __res
         if (!sure) id = choose_exact<NI, L>(row, a, route_rows + (int64_t)warp * a.E, lane);
         // ---- weights: lane j < k has the j-th choice
         const bool mine = lane < a.k && id >= 0;
-        const float lj = mine ? ld_logit(row + id) + 0.0f : NEG;
+        const float lj = mine ? ld_logit(row + id) : NEG;
         float w = 0.0f;
         if (a.score == 1) {
-            float q;
-            sigmoid_pair<float>(lj, w, q);
-            if (!mine) w = 0.0f;
-            if (a.renorm) w = w / (warp_sum(w) + 1e-20f);
+            const float u = expf(-fabsf(lj)), inv = rcp1(1.0f + u);
+            w = !mine ? 0.0f : lj < 0.0f ? u * inv : inv;
+            if (a.renorm) w = __fdividef(w, warp_sum(w) + 1e-20f);
         } else if (a.renorm) {
             const float m = redux_max(lj);
             w = mine ? expf(lj - m) : 0.0f;
             const float s = warp_sum(w);
-            w = mine ? w / s : 0.0f;
+            w = mine ? __fdividef(w, s) : 0.0f;
         } else {
-            w = mine ? expf(lj - top) / sum : 0.0f;
+            w = mine ? __fdividef(expf(lj - top), sum) : 0.0f;
         }
         if (lane < a.k) {
             weights[t * a.k + lane] = w * a.scale;
