@@ -3,17 +3,18 @@
 //
 // ids (n = T * k values in 0..E-1, or out of range: routed nowhere) -> a stable sort by
 // expert: row r of the grouped operand holds slot src[r] (token src[r] / k), group e is
-// rows [offs[e-1], offs[e]), rows[slot] is the slot's row or -1.  Counting sort in two
-// passes over the ids:
-//   count   a CTA per chunk of PL_CHUNK slots: the chunk's count of every expert, to the
-//           workspace, [chunk][E];
-//   scan    (more than one chunk) one warp per 32 experts walks the chunks and replaces
-//           counts by the number of slots of that expert in earlier chunks; the totals
-//           follow in the workspace;
-//   place   a CTA per chunk: expert starts from the totals, then every slot's row = start +
-//           earlier chunks' + earlier warps' + rank within the warp.
-// A warp owns PL_CHUNK / 8 consecutive slots, and ranks among 32 neighbouring slots come
-// from a match of equal ids, so the order is that of the slots and no atomic decides it.
+// rows [offs[e-1], offs[e]), rows[slot] is the slot's row or -1.  A counting sort:
+//   one CTA (n <= PL_ONE) keeps everything in shared memory: every warp counts its run of
+//   consecutive slots by expert, the counts become starts, every slot takes its row.
+//   Else a CTA per chunk of PL_CHUNK slots in three launches, each dependent on the one
+//   before: count writes the chunk's count of every expert to the workspace, [E][chunks];
+//   scan, a warp per expert, turns them into the slots of that expert in earlier chunks,
+//   and its total; place proceeds as the one CTA does, from those.
+// Ranks among 32 neighbouring slots come from a match of equal ids, so the order is that of
+// the slots and no atomic decides it.
+//
+// The bytes (12 per slot) are few: what it costs is the launches and the latency of each
+// step.  524288 slots over 256 experts: see the launcher.
 
 #include <algorithm>
 
@@ -24,83 +25,98 @@ namespace mxq {
 
 namespace {
 
-constexpr int PL_WARPS = 8;
-constexpr int PL_CHUNK = 2048;
-constexpr int PL_STEPS = PL_CHUNK / (32 * PL_WARPS);
+constexpr int PL_CHUNK = 2048, PL_CHUNK_WARPS = 8;  // 256 slots per warp
+constexpr int PL_ONE = 16384, PL_ONE_WARPS = 32;    // at most 512 slots per warp
 
-// Counts of the warp's slots by expert into cnt[0..E) (shared, zeroed by the warp).
-__device__ __forceinline__ void warp_count(const int (&id)[PL_STEPS], int E, int* cnt, int lane) {
+// Slot `at`'s expert, -1 if it has none.
+__device__ __forceinline__ int slot_id(const int32_t* __restrict__ ids, int64_t at, int64_t end, int E) {
+    const int v = at < end ? __ldg(ids + at) : -1;
+    return v < 0 || v >= E ? -1 : v;
+}
+
+// The warp's slots [first, end) by expert, into cnt[0..E) (shared).
+__device__ __forceinline__ void warp_count(const int32_t* __restrict__ ids, int64_t first, int64_t end, int E, int* cnt,
+                                           int lane) {
     for (int e = lane; e < E; e += 32) cnt[e] = 0;
     __syncwarp();
-#pragma unroll
-    for (int i = 0; i < PL_STEPS; ++i) {
-        const unsigned same = __match_any_sync(FULL_MASK, id[i]);
-        if (id[i] >= 0 && lane == __ffs(same) - 1) cnt[id[i]] += __popc(same);
+#pragma unroll 4
+    for (int64_t a = first; a < end; a += 32) {
+        const int id = slot_id(ids, a + lane, end, E);
+        const unsigned same = __match_any_sync(FULL_MASK, id);
+        if (id >= 0 && lane == __ffs(same) - 1) cnt[id] += __popc(same);
         __syncwarp();
     }
 }
 
-__device__ __forceinline__ void load_ids(const int32_t* __restrict__ ids, int64_t n, int E, int64_t first, int lane,
-                                         int (&id)[PL_STEPS]) {
-#pragma unroll
-    for (int i = 0; i < PL_STEPS; ++i) {
-        const int64_t at = first + 32 * i + lane;
-        int v = at < n ? __ldg(ids + at) : -1;
-        if (v < 0 || v >= E) v = -1;
-        id[i] = v;
-    }
-}
-
-__global__ void __launch_bounds__(32 * PL_WARPS) plan_count_kernel(const int32_t* __restrict__ ids, int64_t n, int E,
-                                                                   int32_t* __restrict__ counts) {
+__global__ void __launch_bounds__(32 * PL_CHUNK_WARPS) plan_count_kernel(const int32_t* __restrict__ ids, int64_t n,
+                                                                         int E, int32_t* __restrict__ counts) {
     extern __shared__ int plan_s[];
+    grid_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int id[PL_STEPS];
-    load_ids(ids, n, E, (int64_t)blockIdx.x * PL_CHUNK + warp * (PL_CHUNK / PL_WARPS), lane, id);
-    warp_count(id, E, plan_s + warp * E, lane);
+    const int64_t first = (int64_t)blockIdx.x * PL_CHUNK + warp * (PL_CHUNK / PL_CHUNK_WARPS);
+    warp_count(ids, first, min(n, first + PL_CHUNK / PL_CHUNK_WARPS), E, plan_s + warp * E, lane);
     __syncthreads();
-    for (int e = threadIdx.x; e < E; e += 32 * PL_WARPS) {
+    for (int e = threadIdx.x; e < E; e += 32 * PL_CHUNK_WARPS) {
         int c = 0;
 #pragma unroll
-        for (int w = 0; w < PL_WARPS; ++w) c += plan_s[w * E + e];
-        counts[(int64_t)blockIdx.x * E + e] = c;
+        for (int w = 0; w < PL_CHUNK_WARPS; ++w) c += plan_s[w * E + e];
+        counts[(int64_t)e * gridDim.x + blockIdx.x] = c;
     }
 }
 
-// counts[chunk][e] -> slots of e in earlier chunks; counts[chunks][e] = total.
-__global__ void __launch_bounds__(32) plan_scan_kernel(int32_t* __restrict__ counts, int chunks, int E) {
-    const int e = blockIdx.x * 32 + threadIdx.x;
+// Row e of counts (one warp each) -> its exclusive prefix sums; totals[e] their sum.
+__global__ void __launch_bounds__(128) plan_scan_kernel(int32_t* __restrict__ counts, int chunks, int E,
+                                                        int32_t* __restrict__ totals) {
+    grid_wait();
+    const int lane = threadIdx.x & 31, e = blockIdx.x * 4 + (threadIdx.x >> 5);
     if (e >= E) return;
+    int32_t* row = counts + (int64_t)e * chunks;
     int run = 0;
-    for (int c = 0; c < chunks; ++c) {
-        const int v = counts[(int64_t)c * E + e];
-        counts[(int64_t)c * E + e] = run;
-        run += v;
+    for (int c0 = 0; c0 < chunks; c0 += 128) {
+        int v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int c = c0 + 32 * i + lane;
+            v[i] = c < chunks ? row[c] : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int c = c0 + 32 * i + lane;
+            int inc = v[i];
+#pragma unroll
+            for (int s = 1; s < 32; s <<= 1) {
+                const int o = __shfl_up_sync(FULL_MASK, inc, s);
+                if (lane >= s) inc += o;
+            }
+            if (c < chunks) row[c] = run + inc - v[i];
+            run += __shfl_sync(FULL_MASK, inc, 31);
+        }
     }
-    counts[(int64_t)chunks * E + e] = run;
+    if (lane == 0) totals[e] = run;
 }
 
-// `before` / `totals`: NULL when there is one chunk (both come from its own counts).
-__global__ void __launch_bounds__(32 * PL_WARPS) plan_place_kernel(const int32_t* __restrict__ ids, int64_t n, int E,
-                                                                   const int32_t* __restrict__ before,
-                                                                   const int32_t* __restrict__ totals,
-                                                                   int32_t* __restrict__ offs,
-                                                                   int32_t* __restrict__ rows,
-                                                                   int32_t* __restrict__ src) {
-    extern __shared__ int plan_s[];  // [PL_WARPS][E] counts, then starts; [E] expert starts
+// WARPS warps take `per` consecutive slots each.  before / totals: NULL for the one CTA
+// that has all slots (both come from its own counts).
+template <int WARPS>
+__global__ void __launch_bounds__(32 * WARPS) plan_place_kernel(const int32_t* __restrict__ ids, int64_t n, int per,
+                                                                int E, const int32_t* __restrict__ before,
+                                                                const int32_t* __restrict__ totals,
+                                                                int32_t* __restrict__ offs, int32_t* __restrict__ rows,
+                                                                int32_t* __restrict__ src) {
+    extern __shared__ int plan_s[];  // [WARPS][E] counts, then starts; [E] expert starts
     __shared__ int routed_s;
+    grid_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int* starts = plan_s + PL_WARPS * E;
-    const int64_t first = (int64_t)blockIdx.x * PL_CHUNK + warp * (PL_CHUNK / PL_WARPS);
-    int id[PL_STEPS];
-    load_ids(ids, n, E, first, lane, id);
-    warp_count(id, E, plan_s + warp * E, lane);
+    int* starts = plan_s + WARPS * E;
+    const int64_t first = ((int64_t)blockIdx.x * WARPS + warp) * per, end = min(n, first + per);
+    int* mine = plan_s + warp * E;
+    warp_count(ids, first, end, E, mine, lane);
     __syncthreads();
-    // per expert: turn the warps' counts into starts relative to the chunk, keep its total
-    for (int e = threadIdx.x; e < E; e += 32 * PL_WARPS) {
-        int run = before ? before[(int64_t)blockIdx.x * E + e] : 0;
+    // per expert: the warps' counts become starts relative to the expert's; its total
+    for (int e = threadIdx.x; e < E; e += 32 * WARPS) {
+        int run = before ? before[(int64_t)e * gridDim.x + blockIdx.x] : 0;
 #pragma unroll
-        for (int w = 0; w < PL_WARPS; ++w) {
+        for (int w = 0; w < WARPS; ++w) {
             const int v = plan_s[w * E + e];
             plan_s[w * E + e] = run;
             run += v;
@@ -128,45 +144,56 @@ __global__ void __launch_bounds__(32 * PL_WARPS) plan_place_kernel(const int32_t
         if (lane == 0) routed_s = carry;
     }
     __syncthreads();
-    int* mine = plan_s + warp * E;
-#pragma unroll
-    for (int i = 0; i < PL_STEPS; ++i) {
-        const unsigned same = __match_any_sync(FULL_MASK, id[i]);
-        const int64_t at = first + 32 * i + lane;
+    const int routed = routed_s;
+#pragma unroll 4
+    for (int64_t a = first; a < end; a += 32) {
+        const int64_t at = a + lane;
+        const int id = slot_id(ids, at, end, E);
+        const unsigned same = __match_any_sync(FULL_MASK, id);
         int r = -1;
-        if (id[i] >= 0) r = starts[id[i]] + mine[id[i]] + __popc(same & ((1u << lane) - 1u));
+        if (id >= 0) r = starts[id] + mine[id] + __popc(same & ((1u << lane) - 1u));
         __syncwarp();
-        if (id[i] >= 0 && lane == __ffs(same) - 1) mine[id[i]] += __popc(same);
+        if (id >= 0 && lane == __ffs(same) - 1) mine[id] += __popc(same);
         __syncwarp();
-        if (at < n) {
+        if (at < end) {
             rows[at] = r;
             if (r >= 0) src[r] = (int32_t)at;
-            if (at >= routed_s) src[at] = -1;  // rows behind the last group
+            if (at >= routed) src[at] = -1;  // rows behind the last group
         }
     }
 }
 
+int64_t plan_chunks(int64_t n) { return (n + PL_CHUNK - 1) / PL_CHUNK; }
+
 }  // namespace
 
-// One chunk needs none: its counts never leave the CTA.
-int64_t plan_workspace_bytes(int64_t n, int E) {
-    const int64_t chunks = (n + PL_CHUNK - 1) / PL_CHUNK;
-    return chunks <= 1 ? 0 : 4 * (chunks + 1) * E;
-}
+// The one CTA needs none: its counts never leave it.
+int64_t plan_workspace_bytes(int64_t n, int E) { return n <= PL_ONE ? 0 : 4 * (plan_chunks(n) + 1) * E; }
 
 cudaError_t launch_moe_plan(const int32_t* ids, int64_t n, int E, int32_t* offs, int32_t* rows, int32_t* src,
                             int32_t* ws, cudaStream_t stream) {
-    const int64_t chunks = std::max<int64_t>(1, (n + PL_CHUNK - 1) / PL_CHUNK);
-    const size_t smem = (size_t)(PL_WARPS + 1) * E * sizeof(int);
-    const int threads = 32 * PL_WARPS;
-    if (chunks == 1) {
-        plan_place_kernel<<<1, threads, smem, stream>>>(ids, n, E, nullptr, nullptr, offs, rows, src);
-        return cudaGetLastError();
+    if (n <= PL_ONE) {
+        // a slot per lane and step, at least one step for each warp
+        const size_t smem = (size_t)(PL_ONE_WARPS + 1) * E * sizeof(int);
+        const int per = std::max(32, (int)((n + 32 * PL_ONE_WARPS - 1) / (32 * PL_ONE_WARPS)) * 32);
+        const auto kernel = plan_place_kernel<PL_ONE_WARPS>;
+        if (smem > 48 * 1024) {
+            const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            if (e != cudaSuccess) return e;
+        }
+        return launch_dependent(kernel, 1, 32 * PL_ONE_WARPS, smem, stream, ids, n, per, E, nullptr, nullptr, offs,
+                                rows, src);
     }
-    plan_count_kernel<<<(unsigned)chunks, threads, smem, stream>>>(ids, n, E, ws);
-    plan_scan_kernel<<<(unsigned)((E + 31) / 32), 32, 0, stream>>>(ws, (int)chunks, E);
-    plan_place_kernel<<<(unsigned)chunks, threads, smem, stream>>>(ids, n, E, ws, ws + chunks * E, offs, rows, src);
-    return cudaGetLastError();
+    const int chunks = (int)plan_chunks(n);
+    const size_t smem = (size_t)(PL_CHUNK_WARPS + 1) * E * sizeof(int);
+    int32_t* totals = ws + (int64_t)chunks * E;
+    cudaError_t e = launch_dependent(plan_count_kernel, chunks, 32 * PL_CHUNK_WARPS, smem, stream, ids, n, E, ws);
+    if (e == cudaSuccess)
+        e = launch_dependent(plan_scan_kernel, (E + 3) / 4, 128, 0, stream, ws, chunks, E, totals);
+    if (e == cudaSuccess)
+        e = launch_dependent(plan_place_kernel<PL_CHUNK_WARPS>, chunks, 32 * PL_CHUNK_WARPS, smem, stream, ids, n,
+                             PL_CHUNK / PL_CHUNK_WARPS, E, ws, totals, offs, rows, src);
+    return e;
 }
 
 }  // namespace mxq

@@ -10,6 +10,25 @@ namespace mxq {
 // Number of SMs of the current device (cached per device).
 int sm_count();
 
+// Launch with programmatic dependence on the kernel before it in the stream: the CTAs may
+// become resident before that kernel has ended, so `kernel` begins with grid_wait(), which
+// holds every thread until it has (and its writes are visible).
+template <typename... P, typename... A>
+inline cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                                    A&&... args) {
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 // 2-D tensor map over a row-major bf16 (outer, inner) array: boxes of box_outer rows x
 // box_inner elements, zero fill out of bounds, no swizzle.  False if the driver refuses.
 bool encode_bf16_tile_map(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint32_t box_inner,

@@ -267,7 +267,7 @@ def test_route_many_rows_are_all_written():
 # ---- plan --------------------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("T,k,E", [(0, 4, 8), (1, 1, 1), (1, 8, 128), (7, 3, 5), (256, 8, 16), (255, 8, 300),
-                                   (257, 8, 16), (1000, 6, 1024), (3001, 7, 64), (9000, 2, 3)])
+                                   (257, 8, 16), (1000, 6, 1024), (2048, 8, 256), (2049, 8, 256), (3001, 7, 64), (9000, 2, 3), (40000, 3, 1024)])
 @pytest.mark.parametrize("kind", ["spread", "one", "none", "foreign"])
 def test_plan(T, k, E, kind):
     g = gen(T + E)
@@ -293,8 +293,8 @@ def test_plan(T, k, E, kind):
 
 
 def test_plan_refuses_a_small_workspace():
-    ids = torch.zeros(5000, dtype=torch.int32, device="cuda")
-    out = [torch.empty(n, dtype=torch.int32, device="cuda") for n in (8, 5000, 5000)]
+    ids = torch.zeros(50000, dtype=torch.int32, device="cuda")
+    out = [torch.empty(n, dtype=torch.int32, device="cuda") for n in (8, 50000, 50000)]
     with pytest.raises(mxq.MxqError, match="workspace"):
         mxq.moe_plan(ids, *out)
     with pytest.raises(mxq.MxqError, match="workspace"):
