@@ -373,9 +373,9 @@ const char* mxq_last_cuda_error(void) { return g_last_cuda_error; }
 int mxq_wait_timeouts(unsigned int* count) {
     if (!count) return MXQ_ERR_NULL;
     const unsigned int n = mxq::read_wait_timeouts(), m = mxq::read_gemm_timeouts(),
-                       f = mxq::read_f4_gemm_timeouts();
-    if (n == 0xFFFFFFFFu || m == 0xFFFFFFFFu || f == 0xFFFFFFFFu) return MXQ_ERR_CUDA;
-    *count = n + m + f;
+                       f = mxq::read_f4_gemm_timeouts(), r = mxq::read_norm_timeouts();
+    if (n == 0xFFFFFFFFu || m == 0xFFFFFFFFu || f == 0xFFFFFFFFu || r == 0xFFFFFFFFu) return MXQ_ERR_CUDA;
+    *count = n + m + f + r;
     return MXQ_OK;
 }
 

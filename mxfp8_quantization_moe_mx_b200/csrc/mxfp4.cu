@@ -74,6 +74,10 @@ __global__ void __launch_bounds__(256) f4_quant_kernel(const uint16_t* __restric
     const int64_t gwarp = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
     const int64_t n_warps = (int64_t)gridDim.x * (blockDim.x >> 5);
     for (int64_t base = gwarp * (8 * U); base < n_blocks; base += n_warps * (8 * U)) {
+        {   // L2 prefetch of this warp's next step: 8U blocks of 64 bytes, a line per lane
+            const int64_t nb = base + n_warps * (8 * U) + 2 * lane;
+            if (lane < 4 * U && nb < n_blocks) prefetch_l2(x + nb * 32);
+        }
         uint4 v[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -97,7 +101,7 @@ __global__ void __launch_bounds__(256) f4_quant_kernel(const uint16_t* __restric
 // ---- with scales in the tensor cores' tiles: a CTA per padded 128-row tile x 512 columns
 // (16 scale columns, 4 scale tiles).  Warp w takes rows w, w + 8, ... of the tile, 1024
 // bytes of a row per step; scales gather in shared memory and leave as whole 16-byte lines.
-__global__ void __launch_bounds__(256) f4_quant_blocked_kernel(const uint16_t* __restrict__ x, int64_t rows,
+__global__ void __launch_bounds__(256, 5) f4_quant_blocked_kernel(const uint16_t* __restrict__ x, int64_t rows,
                                                                int64_t cols, uint8_t* __restrict__ q,
                                                                uint8_t* __restrict__ s, uint8_t* __restrict__ sf,
                                                                const int32_t* __restrict__ offs, int32_t G,
@@ -154,27 +158,33 @@ __global__ void __launch_bounds__(256) f4_quant_blocked_kernel(const uint16_t* _
     if (valid < 0) return;
     const int64_t c0 = (int64_t)blockIdx.y * 512;
     const int64_t n_k = cols / 32;
-    for (int r = warp; r < valid; r += 8) {
-        const uint16_t* row = x + (r0 + r) * cols;
-        uint4 v[2];
+    constexpr int R = 2;  // rows of a warp in flight
+    for (int rr = warp; rr < valid; rr += 8 * R) {
+        uint4 v[R][2];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int64_t c = c0 + u * 256 + lane * 8;
-            v[u] = c < cols ? ld_nc_v4(row + c) : make_uint4(0, 0, 0, 0);
-        }
+        for (int i = 0; i < R; ++i)
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int64_t c = c0 + u * 256 + lane * 8;
-            const uint32_t b = f4_scale_of_amax(block_amax(v[u]));
-            const uint32_t code = f4_codes8(v[u], b);
-            if (c < cols) {
-                *reinterpret_cast<uint32_t*>(q + ((r0 + r) * cols + c) / 2) = code;
-                if ((lane & 3) == 0) {
-                    sc[r][u * 8 + (lane >> 2)] = (uint8_t)b;
-                    if (s) s[(r0 + r) * n_k + c / 32] = (uint8_t)b;
+            for (int u = 0; u < 2; ++u) {
+                const int64_t c = c0 + u * 256 + lane * 8;
+                const int r = rr + 8 * i;
+                v[i][u] = r < valid && c < cols ? ld_nc_v4(x + (r0 + r) * cols + c) : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int64_t c = c0 + u * 256 + lane * 8;
+                const int r = rr + 8 * i;
+                const uint32_t b = f4_scale_of_amax(block_amax(v[i][u]));
+                const uint32_t code = f4_codes8(v[i][u], b);
+                if (r < valid && c < cols) {
+                    *reinterpret_cast<uint32_t*>(q + ((r0 + r) * cols + c) / 2) = code;
+                    if ((lane & 3) == 0) {
+                        sc[r][u * 8 + (lane >> 2)] = (uint8_t)b;
+                        if (s) s[(r0 + r) * n_k + c / 32] = (uint8_t)b;
+                    }
                 }
             }
-        }
     }
     __syncthreads();
     if (tid < 128) {
@@ -191,9 +201,10 @@ __global__ void __launch_bounds__(256) f4_quant_blocked_kernel(const uint16_t* _
     }
 }
 
-// ---- dequantize: a lane per half block (8 bytes of codes -> 16 bf16) -------------------------------
+// ---- dequantize: a lane per 8 elements (4 bytes of codes -> one 16-byte store), U steps of
+// a warp in flight
 
-// Two codes (one byte) as a packed pair of f16, exactly.
+// Two codes (the low byte) as fp32, through a packed pair of f16, exactly.
 __device__ __forceinline__ void e2m1x2_to_f32(uint32_t byte, float& a, float& b) {
     asm("{\n\t.reg .b8 c;\n\t.reg .b32 p, t;\n\t.reg .b16 h0, h1;\n\t"
         "mov.b32 {c, _, _, _}, %2;\n\t"
@@ -219,15 +230,24 @@ __device__ __forceinline__ uint4 f4_dequant8(uint32_t codes, uint32_t b) {
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+template <int U>
 __global__ void __launch_bounds__(256) f4_dequant_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ s,
-                                                         uint16_t* __restrict__ y, int64_t n_half) {
-    const int64_t step = (int64_t)gridDim.x * 256;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n_half; i += step) {
-        const uint2 c = ld_nc_v2(q + 8 * i);
-        const uint32_t b = ld_nc_u8(s + (i >> 1));
-        uint4* o = reinterpret_cast<uint4*>(y + 16 * i);
-        o[0] = f4_dequant8(c.x, b);
-        o[1] = f4_dequant8(c.y, b);
+                                                         uint16_t* __restrict__ y, int64_t n8) {
+    const int lane = threadIdx.x & 31;
+    const int64_t gwarp = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5), n_warps = (int64_t)gridDim.x * 8;
+    for (int64_t base = gwarp * (32 * U); base < n8; base += n_warps * (32 * U)) {
+        uint32_t c[U], b[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t i = base + 32 * u + lane;
+            c[u] = i < n8 ? __ldg(reinterpret_cast<const uint32_t*>(q) + i) : 0u;
+            b[u] = i < n8 ? ld_nc_u8(s + (i >> 2)) : 0u;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t i = base + 32 * u + lane;
+            if (i < n8) reinterpret_cast<uint4*>(y)[i] = f4_dequant8(c[u], b[u]);
+        }
     }
 }
 
@@ -254,10 +274,10 @@ cudaError_t launch_f4_quant(const uint16_t* x, int64_t batch, int64_t rows, int6
 }
 
 cudaError_t launch_f4_dequant(const uint8_t* q, const uint8_t* s, uint16_t* y, int64_t n, cudaStream_t stream) {
-    const int64_t n_half = n / 16;
-    const int64_t ctas = (n_half + 255) / 256;
-    f4_dequant_kernel<<<(unsigned)std::min<int64_t>(ctas, (int64_t)sm_count() * 16), 256, 0, stream>>>(q, s, y,
-                                                                                                     n_half);
+    constexpr int U = 4;
+    const int64_t n8 = n / 8;
+    const int64_t ctas = (n8 + 256 * U - 1) / (256 * U);
+    f4_dequant_kernel<U><<<(unsigned)std::min<int64_t>(ctas, (int64_t)sm_count() * 8), 256, 0, stream>>>(q, s, y, n8);
     return cudaGetLastError();
 }
 

@@ -103,6 +103,7 @@ cudaError_t launch_rmsnorm_mx(const uint16_t* x, const uint16_t* residual, const
                               int D, float eps, uint16_t* res_out, uint16_t* y, uint8_t* q, uint8_t* s, float* rstd,
                               cudaStream_t stream);
 int64_t rmsnorm_workspace_bytes(int64_t M, int64_t D);
+unsigned int read_norm_timeouts();
 cudaError_t launch_rmsnorm_backward(const uint16_t* gy, const uint16_t* h, const void* w, bool w_bf16,
                                     const float* rstd, const uint16_t* gres, int64_t M, int D, uint16_t* gx,
                                     float* gw, float* ws, cudaStream_t stream);

@@ -6,16 +6,19 @@
 //   y = bf16(h r w)
 //   q, s = 1x32 MXFP8 blocks of y     (the bytes mx_quantize gives for y)
 //
-// Everything is bound by HBM: a row is read once, stays in registers through the two
-// reductions (sum of squares over the CTA, block maxima over four lanes) and leaves as
-// codes.  A CTA owns a row at a time; thread t holds the 8-element vectors t, t + T, ...,
-// so four neighbouring lanes hold one 32-element block.  The sums are fp32: a thread adds
+// Everything is bound by HBM: a row is read once, by bulk copies into a ring of rows in
+// shared memory, stays in registers through the two reductions (sum of squares over the
+// CTA, block maxima over four lanes) and leaves as codes.  A CTA owns a row at a time; a
+// warp holds 32 V consecutive 8-element vectors of it, lane l the vectors l, l + 32, ..., so
+// four neighbouring lanes hold one 32-element block and a warp's 8 V scale bytes leave in one
+// run.  The sums are fp32: a thread adds
 // at most 32 squares, then 5 shuffle steps and at most 32 warps' sums, so the relative
 // error stays under 2^-18.
 
 #include <algorithm>
 #include <type_traits>
 
+#include "mxq.h"
 #include "mxq_device.cuh"
 #include "mxq_launch.h"
 
@@ -33,32 +36,70 @@ __device__ __forceinline__ uint4 ld_v4(const void* p) {
     return r;
 }
 
-__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
-    f[0] = bf16_lo(v.x), f[1] = bf16_hi(v.x), f[2] = bf16_lo(v.y), f[3] = bf16_hi(v.y);
-    f[4] = bf16_lo(v.z), f[5] = bf16_hi(v.z), f[6] = bf16_lo(v.w), f[7] = bf16_hi(v.w);
+// Two fp32 operations at once (sm_100): d = a b + c, a b.
+struct f2 {
+    float x, y;
+};
+__device__ __forceinline__ unsigned long long pk(f2 v) {
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(v.x), "f"(v.y));
+    return r;
+}
+__device__ __forceinline__ f2 unpk(unsigned long long v) {
+    f2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pk(a)), "l"(pk(b)), "l"(pk(c)));
+    return unpk(r);
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    unsigned long long r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pk(a)), "l"(pk(b)));
+    return unpk(r);
+}
+__device__ __forceinline__ f2 bf2(uint32_t w) { return {bf16_lo(w), bf16_hi(w)}; }
+
+// The i-th pair of a vector of eight bf16.
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+
+// Sums of bf16 pairs, rounded once (the exact sum of two bf16 that an fp32 addition would
+// round first is never near a midpoint of bf16, so this is also bf16(fp32 sum)).
+__device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint4 add8(const uint4& a, const uint4& b) {
+    return make_uint4(add_bf16x2(a.x, b.x), add_bf16x2(a.y, b.y), add_bf16x2(a.z, b.z), add_bf16x2(a.w, b.w));
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-    return make_uint4(cvt_bf16x2(f[0], f[1]), cvt_bf16x2(f[2], f[3]), cvt_bf16x2(f[4], f[5]),
-                      cvt_bf16x2(f[6], f[7]));
-}
-
-// Eight consecutive weights as fp32.
-__device__ __forceinline__ void load_w8(const float* w, float (&f)[8]) {
+// Eight consecutive weights: four pairs as fp32.
+__device__ __forceinline__ void load_w8(const float* w, f2 (&f)[4]) {
     const float4 a = __ldg(reinterpret_cast<const float4*>(w)), b = __ldg(reinterpret_cast<const float4*>(w) + 1);
-    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+    f[0] = {a.x, a.y}, f[1] = {a.z, a.w}, f[2] = {b.x, b.y}, f[3] = {b.z, b.w};
 }
-__device__ __forceinline__ void load_w8(const uint16_t* w, float (&f)[8]) {
-    unpack8(__ldg(reinterpret_cast<const uint4*>(w)), f);
+__device__ __forceinline__ void load_w8(const uint16_t* w, f2 (&f)[4]) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(w));
+    f[0] = bf2(v.x), f[1] = bf2(v.y), f[2] = bf2(v.z), f[3] = bf2(v.w);
+}
+
+// The thread's i-th vector of its V.
+template <int V>
+__device__ __forceinline__ int vec_of(int i) {
+    return ((int)(threadIdx.x >> 5) * V + i) * 32 + (int)(threadIdx.x & 31);
 }
 
 // Sum over the CTA, returned to every thread.  `part` holds 2 x 32 floats; `turn`
-// alternates between calls, so that one barrier a call is enough.
-__device__ __forceinline__ float cta_sum(float v, float* part, int turn) {
+// alternates between calls, so that one barrier a call is enough (none for a single warp,
+// unless it is asked for).
+__device__ __forceinline__ float cta_sum(float v, float* part, int turn, bool barrier = false) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = blockDim.x >> 5;
 #pragma unroll
     for (int s = 16; s; s >>= 1) v += __shfl_xor_sync(FULL_MASK, v, s);
-    if (n == 1) return v;
+    if (n == 1 && !barrier) return v;
     if (lane == 0) part[32 * turn + warp] = v;
     __syncthreads();
     v = lane < n ? part[32 * turn + lane] : 0.0f;
@@ -67,88 +108,199 @@ __device__ __forceinline__ float cta_sum(float v, float* part, int turn) {
     return v;
 }
 
-// V 8-element vectors per thread; D / 8 <= V * blockDim.x.
+// ---- a ring of rows in shared memory --------------------------------------------------------------
+//
+// With many rows a CTA walks rows blockIdx.x, + gridDim.x, ... and bulk copies bring its next
+// rows into shared memory while it works on one, so that the loads in flight do not depend
+// on registers or on how the reductions serialise a row.  Stage s is refilled once the
+// barrier inside the row's reduction has shown that every thread has read it.  A wait that
+// runs out (see mxq_set_wait_limit_ns for how long the library's waits are by default) ends
+// the CTA: it stores nothing more, waits for its copies in flight, and is counted.
+__device__ unsigned int g_norm_timeouts = 0;
+
+constexpr uint64_t NORM_WAIT_NS = MXQ_WAIT_LIMIT_DEFAULT_NS, NORM_DRAIN_NS = 20000000000ull;
+constexpr int NORM_MAX_STAGES = 4;
+
+struct Ring {
+    uint64_t full[NORM_MAX_STAGES];
+    int abort;
+};
+
+// N tensors' rows side by side in a stage of N * D bf16.
+template <int N>
+__device__ __forceinline__ void ring_fill(uint8_t* sm, Ring* ring, int st, const uint16_t* const (&from)[3], int64_t at,
+                                          int D) {
+    mbar_arrive_expect_tx(&ring->full[st], (uint32_t)(N * D * 2));
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        bulk_load(sm + ((size_t)st * N + i) * D * 2, from[i] + at, (uint32_t)(D * 2), &ring->full[st]);
+}
+
+template <int N>
+__device__ __forceinline__ void ring_start(uint8_t* sm, Ring* ring, int stages, const uint16_t* const (&from)[3],
+                                           int64_t M, int D) {
+    if (threadIdx.x == 0) {
+        ring->abort = 0;
+        for (int st = 0; st < stages; ++st) mbar_init(&ring->full[st], 1);
+        for (int st = 0; st < stages; ++st) {
+            const int64_t m = blockIdx.x + (int64_t)st * gridDim.x;
+            if (m < M) ring_fill<N>(sm, ring, st, from, m * D, D);
+        }
+    }
+    __syncthreads();
+}
+
+// After an abort at row m of stage st: thread 0 waits for the copies of the rows that were
+// in flight (this one's and the stages' after it).
+__device__ __forceinline__ void ring_leave(Ring* ring, int stages, int st, uint32_t phase, int64_t m, int64_t M) {
+    if (threadIdx.x != 0) return;
+    for (int i = 0; i < stages && m < M; ++i, m += gridDim.x) {
+        mbar_wait_bounded(&ring->full[st], phase, NORM_DRAIN_NS);
+        if (++st == stages) {
+            st = 0;
+            phase ^= 1;
+        }
+    }
+    atomicAdd(&g_norm_timeouts, 1u);
+}
+
+// One row's norm and codes from its packed sums h[] (V vectors per thread), stored.
 template <int V, typename W>
-__global__ void __launch_bounds__(V == 1 ? 1024 : 512) rmsnorm_mx_kernel(
-    const uint16_t* x, const uint16_t* residual, const W* __restrict__ w, int64_t M, int D, float eps,
-    uint16_t* res_out, uint16_t* y, uint8_t* __restrict__ q, uint8_t* __restrict__ s, float* __restrict__ rstd) {
+__device__ __forceinline__ void norm_row(const uint4 (&h)[V], const W* __restrict__ w, float r, int64_t at, int nv,
+                                         uint16_t* y, uint8_t* __restrict__ q, uint8_t* __restrict__ s) {
+    const int lane = threadIdx.x & 31;
+    uint32_t mine = 0;  // lane l < 8 V: the scale of the warp's block l
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int v = vec_of<V>(i);
+        f2 g[4] = {};
+        if (v < nv) load_w8(w + 8 * v, g);
+        uint32_t p[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const f2 f = mul2(mul2(bf2(word(h[i], j)), f2{r, r}), g[j]);
+            p[j] = cvt_bf16x2(f.x, f.y);
+        }
+        const uint4 o = make_uint4(p[0], p[1], p[2], p[3]);
+        uint32_t am = mag2(amax2(amax2(o.x, o.y), amax2(o.z, o.w)));
+        am = max(am & 0xFFFFu, am >> 16);
+        am = max(am, __shfl_xor_sync(FULL_MASK, am, 1));
+        am = max(am, __shfl_xor_sync(FULL_MASK, am, 2));
+        const uint32_t b = e8m0_of_amax(am);
+        uint2 c;
+        if (b != 255u) {
+            const float mul = mx_mult(b);
+            c.x = quant4(o.x, o.y, mul);
+            c.y = quant4(o.z, o.w, mul);
+        } else {
+            c.x = nan4(o.x, o.y);
+            c.y = nan4(o.z, o.w);
+        }
+        if (v < nv) {
+            if (y) *reinterpret_cast<uint4*>(y + at + 8 * v) = o;
+            *reinterpret_cast<uint2*>(q + at + 8 * v) = c;
+        }
+        const uint32_t t = __shfl_sync(FULL_MASK, b, (lane & 7) * 4);
+        if ((lane >> 3) == i) mine = t;
+    }
+    const int block = (int)(threadIdx.x >> 5) * 8 * V + lane;
+    if (lane < 8 * V && block < nv / 4) s[(at >> 5) + block] = (uint8_t)mine;
+}
+
+template <int V>
+__device__ __forceinline__ float sum_squares(const uint4 (&h)[V]) {
+    f2 sq = {0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const f2 f = bf2(word(h[i], j));
+            sq = fma2(f, f, sq);
+        }
+    return sq.x + sq.y;
+}
+
+// Few rows: a CTA per row, V vectors per thread straight from global memory (two for the
+// rows of more than 8192 elements).
+template <int V, typename W>
+__global__ void __launch_bounds__(1024) rmsnorm_mx_few_kernel(const uint16_t* x, const uint16_t* residual,
+                                                              const W* __restrict__ w, int64_t M, int D, float eps,
+                                                              uint16_t* res_out, uint16_t* y, uint8_t* __restrict__ q,
+                                                              uint8_t* __restrict__ s, float* __restrict__ rstd) {
     __shared__ float part[64];
-    const int tid = threadIdx.x, T = blockDim.x, nv = D / 8;
-    int turn = 0;
+    grid_wait();
+    const int nv = D / 8;
+    const int64_t m = blockIdx.x, at = m * D;
+    uint4 h[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int v = vec_of<V>(i);
+        h[i] = v < nv ? ld_v4(x + at + 8 * v) : make_uint4(0, 0, 0, 0);
+        if (residual && v < nv) h[i] = add8(h[i], ld_v4(residual + at + 8 * v));
+    }
+    if (res_out) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int v = vec_of<V>(i);
+            if (v < nv) *reinterpret_cast<uint4*>(res_out + at + 8 * v) = h[i];
+        }
+    }
+    const float r = __frsqrt_rn(cta_sum(sum_squares<V>(h), part, 0) / (float)D + eps);
+    if (rstd && threadIdx.x == 0) rstd[m] = r;
+    norm_row<V, W>(h, w, r, at, nv, y, q, s);
+}
+
+// Many rows.  V 8-element vectors per thread; D / 8 <= V * blockDim.x; RES: with a residual.
+template <int V, typename W, bool RES>
+__global__ void __launch_bounds__(512) rmsnorm_mx_kernel(const uint16_t* x, const uint16_t* residual,
+                                                         const W* __restrict__ w, int64_t M, int D, float eps,
+                                                         uint16_t* res_out, uint16_t* y, uint8_t* __restrict__ q,
+                                                         uint8_t* __restrict__ s, float* __restrict__ rstd,
+                                                         int stages) {
+    constexpr int N = RES ? 2 : 1;
+    extern __shared__ __align__(128) uint8_t norm_sm[];
+    __shared__ Ring ring;
+    __shared__ float part[64];
+    grid_wait();
+    const int tid = threadIdx.x, nv = D / 8;
+    const uint16_t* const from[3] = {x, residual, nullptr};
+    ring_start<N>(norm_sm, &ring, stages, from, M, D);
+    int st = 0, turn = 0;
+    uint32_t phase = 0;
     for (int64_t m = blockIdx.x; m < M; m += gridDim.x, turn ^= 1) {
         const int64_t at = m * D;
+        if (!mbar_wait_bounded(&ring.full[st], phase, NORM_WAIT_NS)) ring.abort = 1;
+        const uint8_t* row = norm_sm + (size_t)st * N * D * 2;
         uint4 h[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int v = tid + i * T;
-            h[i] = v < nv ? ld_v4(x + at + 8 * v) : make_uint4(0, 0, 0, 0);
+            const int v = vec_of<V>(i);
+            h[i] = v < nv ? lds_v4(row + 16 * v) : make_uint4(0, 0, 0, 0);
+            if (RES && v < nv) h[i] = add8(h[i], lds_v4(row + 2 * D + 16 * v));
         }
-        if (residual) {
-            uint4 a[V];
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int v = tid + i * T;
-                a[i] = v < nv ? ld_v4(residual + at + 8 * v) : make_uint4(0, 0, 0, 0);
-            }
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                float f[8], g[8];
-                unpack8(h[i], f);
-                unpack8(a[i], g);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) f[j] += g[j];
-                h[i] = pack8(f);
-            }
+        const float sum = cta_sum(sum_squares<V>(h), part, turn, true);  // with a barrier: the stage is read
+        if (*(volatile int*)&ring.abort) {
+            ring_leave(&ring, stages, st, phase, m, M);
+            return;
+        }
+        if (tid == 0) {
+            const int64_t next = m + (int64_t)stages * gridDim.x;
+            if (next < M) ring_fill<N>(norm_sm, &ring, st, from, next * D, D);
+        }
+        if (++st == stages) {
+            st = 0;
+            phase ^= 1;
         }
         if (res_out) {
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const int v = tid + i * T;
+                const int v = vec_of<V>(i);
                 if (v < nv) *reinterpret_cast<uint4*>(res_out + at + 8 * v) = h[i];
             }
         }
-        float sq = 0.0f;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            float f[8];
-            unpack8(h[i], f);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) sq = fmaf(f[j], f[j], sq);
-        }
-        const float r = __frsqrt_rn(cta_sum(sq, part, turn) / (float)D + eps);
+        const float r = __frsqrt_rn(sum / (float)D + eps);
         if (rstd && tid == 0) rstd[m] = r;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int v = tid + i * T;
-            float f[8], g[8];
-            unpack8(h[i], f);
-            if (v < nv) load_w8(w + 8 * v, g);
-            else
-#pragma unroll
-                for (int j = 0; j < 8; ++j) g[j] = 0.0f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = f[j] * r * g[j];
-            const uint4 o = pack8(f);
-            uint32_t am = mag2(amax2(amax2(o.x, o.y), amax2(o.z, o.w)));
-            am = max(am & 0xFFFFu, am >> 16);
-            am = max(am, __shfl_xor_sync(FULL_MASK, am, 1));
-            am = max(am, __shfl_xor_sync(FULL_MASK, am, 2));
-            const uint32_t b = e8m0_of_amax(am);
-            uint2 c;
-            if (b != 255u) {
-                const float mul = mx_mult(b);
-                c.x = quant4(o.x, o.y, mul);
-                c.y = quant4(o.z, o.w, mul);
-            } else {
-                c.x = nan4(o.x, o.y);
-                c.y = nan4(o.z, o.w);
-            }
-            if (v < nv) {
-                if (y) *reinterpret_cast<uint4*>(y + at + 8 * v) = o;
-                *reinterpret_cast<uint2*>(q + at + 8 * v) = c;
-                if ((v & 3) == 0) s[(at >> 5) + (v >> 2)] = (uint8_t)b;
-            }
-        }
+        norm_row<V, W>(h, w, r, at, nv, y, q, s);
     }
 }
 
@@ -158,164 +310,202 @@ __global__ void __launch_bounds__(V == 1 ? 1024 : 512) rmsnorm_mx_kernel(
 // A CTA walks rows blockIdx.x, + gridDim.x, ... and keeps its share of gw in registers
 // (fp32), writes it to its row of the workspace, and a second kernel adds the CTAs' rows in
 // order: no atomics, the same bits every time.
-template <int V, typename W>
-__global__ void __launch_bounds__(V == 1 ? 1024 : 512) rmsnorm_backward_kernel(
+template <int V, typename W, bool RES>
+__global__ void __launch_bounds__(512) rmsnorm_backward_kernel(
     const uint16_t* gy, const uint16_t* __restrict__ h, const W* __restrict__ w, const float* __restrict__ rstd,
-    const uint16_t* gres, int64_t M, int D, uint16_t* gx, float* __restrict__ partial) {
+    const uint16_t* gres, int64_t M, int D, uint16_t* gx, float* __restrict__ partial, int stages) {
+    constexpr int N = RES ? 3 : 2;
+    extern __shared__ __align__(128) uint8_t norm_sm[];
+    __shared__ Ring ring;
     __shared__ float part[64];
-    const int tid = threadIdx.x, T = blockDim.x, nv = D / 8;
-    float gw[V][8];
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) gw[i][j] = 0.0f;
-    int turn = 0;
+    grid_wait();
+    const int tid = threadIdx.x, nv = D / 8;
+    const uint16_t* const from[3] = {gy, h, gres};
+    ring_start<N>(norm_sm, &ring, stages, from, M, D);
+    f2 gw[V][4] = {};
+    int st = 0, turn = 0;
+    uint32_t phase = 0;
     for (int64_t m = blockIdx.x; m < M; m += gridDim.x, turn ^= 1) {
         const int64_t at = m * D;
-        uint4 a[V], b[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int v = tid + i * T;
-            a[i] = v < nv ? ld_v4(gy + at + 8 * v) : make_uint4(0, 0, 0, 0);
-            b[i] = v < nv ? ld_nc_v4(h + at + 8 * v) : make_uint4(0, 0, 0, 0);
-        }
         const float r = __ldg(rstd + m);
-        float dot = 0.0f;
+        if (!mbar_wait_bounded(&ring.full[st], phase, NORM_WAIT_NS)) ring.abort = 1;
+        const uint8_t* row = norm_sm + (size_t)st * N * D * 2;
+        uint4 a[V], b[V], e[V];
+        f2 dot = {0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int v = tid + i * T;
-            float f[8], n[8], g[8];
-            unpack8(a[i], f);
-            unpack8(b[i], n);
-            if (v < nv) load_w8(w + 8 * v, g);
-            else
-#pragma unroll
-                for (int j = 0; j < 8; ++j) g[j] = 0.0f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                n[j] *= r;
-                gw[i][j] = fmaf(f[j], n[j], gw[i][j]);
-                dot = fmaf(f[j] * g[j], n[j], dot);
-            }
-        }
-        const float mean = cta_sum(dot, part, turn) / (float)D;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int v = tid + i * T;
+            const int v = vec_of<V>(i);
+            a[i] = b[i] = e[i] = make_uint4(0, 0, 0, 0);
             if (v >= nv) continue;
-            float f[8], n[8], g[8], o[8];
-            unpack8(a[i], f);
-            unpack8(b[i], n);
+            a[i] = lds_v4(row + 16 * v);
+            b[i] = lds_v4(row + 2 * D + 16 * v);
+            if (RES) e[i] = lds_v4(row + 4 * D + 16 * v);
+            f2 g[4];
             load_w8(w + 8 * v, g);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] = r * (f[j] * g[j] - n[j] * r * mean);
-            if (gres) {
-                unpack8(ld_v4(gres + at + 8 * v), f);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) o[j] += f[j];
+            for (int j = 0; j < 4; ++j) {
+                const f2 f = bf2(word(a[i], j)), n = mul2(bf2(word(b[i], j)), f2{r, r});
+                gw[i][j] = fma2(f, n, gw[i][j]);
+                dot = fma2(mul2(f, g[j]), n, dot);
             }
-            *reinterpret_cast<uint4*>(gx + at + 8 * v) = pack8(o);
+        }
+        const float mean = cta_sum(dot.x + dot.y, part, turn, true) / (float)D;  // with a barrier: the stage is read
+        if (*(volatile int*)&ring.abort) {
+            ring_leave(&ring, stages, st, phase, m, M);
+            return;
+        }
+        if (tid == 0) {
+            const int64_t next = m + (int64_t)stages * gridDim.x;
+            if (next < M) ring_fill<N>(norm_sm, &ring, st, from, next * D, D);
+        }
+        if (++st == stages) {
+            st = 0;
+            phase ^= 1;
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int v = vec_of<V>(i);
+            if (v >= nv) continue;
+            f2 g[4];
+            load_w8(w + 8 * v, g);
+            uint32_t o[4];
+            const float k = -r * r * mean;  // r (f g - n mean) = f g r - h r^2 mean
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                f2 t = mul2(mul2(bf2(word(a[i], j)), g[j]), f2{r, r});
+                t = fma2(bf2(word(b[i], j)), f2{k, k}, t);
+                if (RES) t = fma2(bf2(word(e[i], j)), f2{1.0f, 1.0f}, t);
+                o[j] = cvt_bf16x2(t.x, t.y);
+            }
+            *reinterpret_cast<uint4*>(gx + at + 8 * v) = make_uint4(o[0], o[1], o[2], o[3]);
         }
     }
     float* mine = partial + (int64_t)blockIdx.x * D;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int v = tid + i * T;
+        const int v = vec_of<V>(i);
         if (v >= nv) continue;
-        *reinterpret_cast<float4*>(mine + 8 * v) = make_float4(gw[i][0], gw[i][1], gw[i][2], gw[i][3]);
-        *reinterpret_cast<float4*>(mine + 8 * v + 4) = make_float4(gw[i][4], gw[i][5], gw[i][6], gw[i][7]);
+        *reinterpret_cast<float4*>(mine + 8 * v) = make_float4(gw[i][0].x, gw[i][0].y, gw[i][1].x, gw[i][1].y);
+        *reinterpret_cast<float4*>(mine + 8 * v + 4) = make_float4(gw[i][2].x, gw[i][2].y, gw[i][3].x, gw[i][3].y);
     }
 }
 
-// gw[d] = sum over the n rows of partial, in a fixed order: warp y of the CTA adds rows
-// y, y + 8, ..., then the eight sums are added in order.
-__global__ void __launch_bounds__(256) rmsnorm_gw_kernel(const float* __restrict__ partial, int n, int D,
-                                                         float* __restrict__ gw) {
-    __shared__ float sums[8][32];
+// gw[d] = sum over the n rows of partial, in a fixed order: warp i of the CTA adds rows
+// i, i + 16, ..., then the sixteen sums are added in order.
+constexpr int GW_WARPS = 16;
+__global__ void __launch_bounds__(32 * GW_WARPS) rmsnorm_gw_kernel(const float* __restrict__ partial, int n, int D,
+                                                                   float* __restrict__ gw) {
+    __shared__ float sums[GW_WARPS][32];
+    grid_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int d = blockIdx.x * 32 + lane;
     float v = 0.0f;
-    for (int r = warp; r < n; r += 8) v += partial[(int64_t)r * D + d];
+#pragma unroll 8
+    for (int r = warp; r < n; r += GW_WARPS) v += partial[(int64_t)r * D + d];
     sums[warp][lane] = v;
     __syncthreads();
     if (warp == 0) {
 #pragma unroll
-        for (int i = 1; i < 8; ++i) v += sums[i][lane];
+        for (int i = 1; i < GW_WARPS; ++i) v += sums[i][lane];
         gw[d] = v;
     }
 }
 
-struct NormShape {
-    int v, threads;
-};
-
-// Threads and vectors per thread for a row of D elements: one vector per thread while that
-// fits in 1024 threads and rows are few, more per thread otherwise.
-NormShape norm_shape(int64_t M, int D) {
-    const int nv = D / 8;
-    const int v = nv <= 32 ? 1 : nv <= 1024 && M <= 2 * (int64_t)sm_count() ? 1 : nv <= 64 ? 2 : 4;
-    const int per = (nv + v - 1) / v;
-    return {v, (per + 31) / 32 * 32};  // at most 1024 for v = 1, 512 for v = 4 (D <= 16384)
-}
-
 constexpr int NORM_MAX_CTAS = 592;
 
+// Four vectors per thread (fewer for short rows).
+int norm_vectors(int nv) { return nv <= 32 ? 1 : nv <= 64 ? 2 : 4; }
+
+// A ring kernel over M rows: two stages at first, as many CTAs per SM as then fit, and what
+// shared memory they leave goes to more stages.  *grid: the CTAs launched (at most max_ctas).
+template <typename K, typename... A>
+cudaError_t launch_ring(K kernel, int v, int tensors, int64_t M, int D, int64_t max_ctas, unsigned* grid,
+                        cudaStream_t stream, const A&... args) {
+    const int nv = D / 8, threads = (nv + 32 * v - 1) / (32 * v) * 32;
+    const int stage = tensors * D * 2;
+    constexpr int TOTAL = 220 * 1024;  // of an SM, with the CTAs' own use (1.5 KB each) left aside
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * stage);
+    int per_sm = 0;
+    if (e == cudaSuccess)
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, (size_t)2 * stage);
+    if (e != cudaSuccess) return e;
+    per_sm = std::max(1, per_sm);
+    const int stages = std::max(2, std::min(NORM_MAX_STAGES, (TOTAL / per_sm - 2048) / stage));
+    if (stages > 2) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, stages * stage);
+        if (e != cudaSuccess) return e;
+    }
+    *grid = (unsigned)std::min({M, (int64_t)sm_count() * per_sm, max_ctas});
+    return launch_dependent(kernel, *grid, threads, (size_t)stages * stage, stream, args..., stages);
+}
+
+template <typename W>
+cudaError_t norm_forward(const uint16_t* x, const uint16_t* residual, const W* w, int64_t M, int D, float eps,
+                         uint16_t* res_out, uint16_t* y, uint8_t* q, uint8_t* s, float* rstd, cudaStream_t stream) {
+    const int nv = D / 8, v = norm_vectors(nv);
+    if (M <= 2 * (int64_t)sm_count()) {
+        return nv <= 1024 ? launch_dependent(rmsnorm_mx_few_kernel<1, W>, (unsigned)M, (nv + 31) / 32 * 32, 0, stream,
+                                             x, residual, w, M, D, eps, res_out, y, q, s, rstd)
+                          : launch_dependent(rmsnorm_mx_few_kernel<2, W>, (unsigned)M, (nv + 63) / 64 * 32, 0, stream,
+                                             x, residual, w, M, D, eps, res_out, y, q, s, rstd);
+    }
+    unsigned grid = 0;
+    auto go = [&](auto vv) {
+        constexpr int V = decltype(vv)::value;
+        return residual ? launch_ring(rmsnorm_mx_kernel<V, W, true>, V, 2, M, D, INT32_MAX, &grid, stream, x, residual,
+                                      w, M, D, eps, res_out, y, q, s, rstd)
+                        : launch_ring(rmsnorm_mx_kernel<V, W, false>, V, 1, M, D, INT32_MAX, &grid, stream, x,
+                                      residual, w, M, D, eps, res_out, y, q, s, rstd);
+    };
+    return v == 1   ? go(std::integral_constant<int, 1>())
+           : v == 2 ? go(std::integral_constant<int, 2>())
+                    : go(std::integral_constant<int, 4>());
+}
+
+template <typename W>
+cudaError_t norm_backward(const uint16_t* gy, const uint16_t* h, const W* w, const float* rstd, const uint16_t* gres,
+                          int64_t M, int D, uint16_t* gx, float* gw, float* ws, cudaStream_t stream) {
+    unsigned grid = 0;
+    if (M > 0) {
+        const int v = norm_vectors(D / 8);
+        auto go = [&](auto vv) {
+            constexpr int V = decltype(vv)::value;
+            return gres ? launch_ring(rmsnorm_backward_kernel<V, W, true>, V, 3, M, D, NORM_MAX_CTAS, &grid, stream,
+                                      gy, h, w, rstd, gres, M, D, gx, ws)
+                        : launch_ring(rmsnorm_backward_kernel<V, W, false>, V, 2, M, D, NORM_MAX_CTAS, &grid, stream,
+                                      gy, h, w, rstd, gres, M, D, gx, ws);
+        };
+        const cudaError_t e = v == 1   ? go(std::integral_constant<int, 1>())
+                              : v == 2 ? go(std::integral_constant<int, 2>())
+                                       : go(std::integral_constant<int, 4>());
+        if (e != cudaSuccess) return e;
+    }
+    return launch_dependent(rmsnorm_gw_kernel, (unsigned)(D / 32), 32 * GW_WARPS, 0, stream, ws, (int)grid, D, gw);
+}
+
 }  // namespace
+
+unsigned int read_norm_timeouts() {
+    unsigned int n = 0;
+    if (cudaMemcpyFromSymbol(&n, g_norm_timeouts, sizeof(n)) != cudaSuccess) return 0xFFFFFFFFu;
+    return n;
+}
 
 int64_t rmsnorm_workspace_bytes(int64_t M, int64_t D) { return 4 * D * std::min<int64_t>(M, NORM_MAX_CTAS); }
 
 cudaError_t launch_rmsnorm_mx(const uint16_t* x, const uint16_t* residual, const void* w, bool w_bf16, int64_t M,
                               int D, float eps, uint16_t* res_out, uint16_t* y, uint8_t* q, uint8_t* s, float* rstd,
                               cudaStream_t stream) {
-    const NormShape sh = norm_shape(M, D);
-    const int per_sm = std::max(1, 1536 / sh.threads);
-    const unsigned grid = (unsigned)std::min<int64_t>(M, (int64_t)sm_count() * per_sm);
-    auto go = [&](auto vv) {
-        constexpr int V = decltype(vv)::value;
-        if (w_bf16)
-            rmsnorm_mx_kernel<V, uint16_t><<<grid, sh.threads, 0, stream>>>(
-                x, residual, static_cast<const uint16_t*>(w), M, D, eps, res_out, y, q, s, rstd);
-        else
-            rmsnorm_mx_kernel<V, float><<<grid, sh.threads, 0, stream>>>(x, residual, static_cast<const float*>(w), M,
-                                                                         D, eps, res_out, y, q, s, rstd);
-        return cudaGetLastError();
-    };
-    switch (sh.v) {
-        case 1: return go(std::integral_constant<int, 1>());
-        case 2: return go(std::integral_constant<int, 2>());
-        default: return go(std::integral_constant<int, 4>());
-    }
+    return w_bf16 ? norm_forward(x, residual, static_cast<const uint16_t*>(w), M, D, eps, res_out, y, q, s, rstd,
+                                 stream)
+                  : norm_forward(x, residual, static_cast<const float*>(w), M, D, eps, res_out, y, q, s, rstd, stream);
 }
 
 cudaError_t launch_rmsnorm_backward(const uint16_t* gy, const uint16_t* h, const void* w, bool w_bf16,
                                     const float* rstd, const uint16_t* gres, int64_t M, int D, uint16_t* gx,
                                     float* gw, float* ws, cudaStream_t stream) {
-    if (M > 0) {
-        const NormShape sh = norm_shape(M, D);
-        const int per_sm = std::max(1, std::min(4, 1024 / sh.threads));
-        const unsigned grid = (unsigned)std::min({M, (int64_t)sm_count() * per_sm, (int64_t)NORM_MAX_CTAS});
-        auto go = [&](auto vv) {
-            constexpr int V = decltype(vv)::value;
-            if (w_bf16)
-                rmsnorm_backward_kernel<V, uint16_t><<<grid, sh.threads, 0, stream>>>(
-                    gy, h, static_cast<const uint16_t*>(w), rstd, gres, M, D, gx, ws);
-            else
-                rmsnorm_backward_kernel<V, float><<<grid, sh.threads, 0, stream>>>(
-                    gy, h, static_cast<const float*>(w), rstd, gres, M, D, gx, ws);
-            return cudaGetLastError();
-        };
-        cudaError_t e;
-        switch (sh.v) {
-            case 1: e = go(std::integral_constant<int, 1>()); break;
-            case 2: e = go(std::integral_constant<int, 2>()); break;
-            default: e = go(std::integral_constant<int, 4>()); break;
-        }
-        if (e != cudaSuccess) return e;
-        rmsnorm_gw_kernel<<<(unsigned)(D / 32), 256, 0, stream>>>(ws, (int)grid, D, gw);
-    } else {
-        rmsnorm_gw_kernel<<<(unsigned)(D / 32), 256, 0, stream>>>(ws, 0, D, gw);
-    }
-    return cudaGetLastError();
+    return w_bf16 ? norm_backward(gy, h, static_cast<const uint16_t*>(w), rstd, gres, M, D, gx, gw, ws, stream)
+                  : norm_backward(gy, h, static_cast<const float*>(w), rstd, gres, M, D, gx, gw, ws, stream);
 }
 
 }  // namespace mxq
