@@ -6,15 +6,17 @@
 // rows [offs[e-1], offs[e]), rows[slot] is the slot's row or -1.  A counting sort:
 //   one CTA (n <= PL_ONE) keeps everything in shared memory: every warp counts its run of
 //   consecutive slots by expert, the counts become starts, every slot takes its row.
-//   Else a CTA per chunk of PL_CHUNK slots in three launches, each dependent on the one
-//   before: count writes the chunk's count of every expert to the workspace, [E][chunks];
-//   scan, a warp per expert, turns them into the slots of that expert in earlier chunks,
-//   and its total; place proceeds as the one CTA does, from those.
-// Ranks among 32 neighbouring slots come from a match of equal ids, so the order is that of
-// the slots and no atomic decides it.
+//   Else CTAs take consecutive chunks of slots in two launches, the second dependent on the
+//   first: count writes the chunks' counts to the workspace, [E][chunks]; place reads them
+//   all (at most 148 chunks, a warp per expert), adds up those of the
+//   earlier chunks and of all, and goes on as the one CTA does.
+// Counting is by shared-memory atomics, whose order does not show.  Ranks among 32
+// neighbouring slots come from a word per expert in which each lane sets its bit, so the
+// rows are in the order of the slots and no atomic decides them (a match of equal ids
+// instead, __match_any_sync, cost 30 us for 22: its time grows with the distinct values).
 //
 // The bytes (12 per slot) are few: what it costs is the launches and the latency of each
-// step.  524288 slots over 256 experts: see the launcher.
+// step.
 
 #include <algorithm>
 
@@ -25,103 +27,112 @@ namespace mxq {
 
 namespace {
 
-constexpr int PL_CHUNK = 2048, PL_CHUNK_WARPS = 8;  // 256 slots per warp
-constexpr int PL_ONE = 16384, PL_ONE_WARPS = 32;    // at most 512 slots per warp
+constexpr int PL_WARPS = 16;
+constexpr int PL_ONE = 8192;        // slots that one CTA takes, at most 512 per warp
+constexpr int PL_MIN_PER = 128;     // more: at least 128 slots per warp, ...
+constexpr int PL_MAX_CHUNKS = 148;  // ... in at most one CTA per SM
 
-// Slot `at`'s expert, -1 if it has none.
-__device__ __forceinline__ int slot_id(const int32_t* __restrict__ ids, int64_t at, int64_t end, int E) {
-    const int v = at < end ? __ldg(ids + at) : -1;
-    return v < 0 || v >= E ? -1 : v;
+constexpr int PL_BATCH = 8;  // steps of 32 slots whose ids are loaded together
+
+// The experts of the lane's slots first + lane, + 32, ... below end; -1 where there is none.
+__device__ __forceinline__ void load_batch(const int32_t* __restrict__ ids, int64_t first, int64_t end, int E,
+                                           int lane, int (&id)[PL_BATCH]) {
+#pragma unroll
+    for (int i = 0; i < PL_BATCH; ++i) {
+        const int64_t at = first + 32 * i + lane;
+        id[i] = at < end ? __ldg(ids + at) : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < PL_BATCH; ++i)
+        if (id[i] >= E) id[i] = -1;
 }
 
-// The warp's slots [first, end) by expert, into cnt[0..E) (shared).
-__device__ __forceinline__ void warp_count(const int32_t* __restrict__ ids, int64_t first, int64_t end, int E, int* cnt,
-                                           int lane) {
-    for (int e = lane; e < E; e += 32) cnt[e] = 0;
-    __syncwarp();
-#pragma unroll 4
-    for (int64_t a = first; a < end; a += 32) {
-        const int id = slot_id(ids, a + lane, end, E);
-        const unsigned same = __match_any_sync(FULL_MASK, id);
-        if (id >= 0 && lane == __ffs(same) - 1) cnt[id] += __popc(same);
-        __syncwarp();
+// The warp's slots [first, end) by expert, added to cnt[0..E) (shared).
+__device__ __forceinline__ void count_slots(const int32_t* __restrict__ ids, int64_t first, int64_t end, int E,
+                                            int* cnt, int lane) {
+    for (int64_t a = first; a < end; a += 32 * PL_BATCH) {
+        int id[PL_BATCH];
+        load_batch(ids, a, end, E, lane, id);
+#pragma unroll
+        for (int i = 0; i < PL_BATCH; ++i)
+            if (id[i] >= 0) atomicAdd(cnt + id[i], 1);
     }
 }
 
-__global__ void __launch_bounds__(32 * PL_CHUNK_WARPS) plan_count_kernel(const int32_t* __restrict__ ids, int64_t n,
-                                                                         int E, int32_t* __restrict__ counts) {
+__global__ void __launch_bounds__(32 * PL_WARPS) plan_count_kernel(const int32_t* __restrict__ ids, int64_t n, int per,
+                                                                   int E, int32_t* __restrict__ counts) {
     extern __shared__ int plan_s[];
     grid_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t first = (int64_t)blockIdx.x * PL_CHUNK + warp * (PL_CHUNK / PL_CHUNK_WARPS);
-    warp_count(ids, first, min(n, first + PL_CHUNK / PL_CHUNK_WARPS), E, plan_s + warp * E, lane);
+    for (int e = threadIdx.x; e < E; e += 32 * PL_WARPS) plan_s[e] = 0;
     __syncthreads();
-    for (int e = threadIdx.x; e < E; e += 32 * PL_CHUNK_WARPS) {
-        int c = 0;
-#pragma unroll
-        for (int w = 0; w < PL_CHUNK_WARPS; ++w) c += plan_s[w * E + e];
-        counts[(int64_t)e * gridDim.x + blockIdx.x] = c;
-    }
+    const int64_t first = ((int64_t)blockIdx.x * PL_WARPS + warp) * per;
+    count_slots(ids, first, min(n, first + per), E, plan_s, lane);
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += 32 * PL_WARPS) counts[(int64_t)e * gridDim.x + blockIdx.x] = plan_s[e];
 }
 
-// Row e of counts (one warp each) -> its exclusive prefix sums; totals[e] their sum.
-__global__ void __launch_bounds__(128) plan_scan_kernel(int32_t* __restrict__ counts, int chunks, int E,
-                                                        int32_t* __restrict__ totals) {
-    grid_wait();
-    const int lane = threadIdx.x & 31, e = blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (e >= E) return;
-    int32_t* row = counts + (int64_t)e * chunks;
-    int run = 0;
-    for (int c0 = 0; c0 < chunks; c0 += 128) {
-        int v[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int c = c0 + 32 * i + lane;
-            v[i] = c < chunks ? row[c] : 0;
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int c = c0 + 32 * i + lane;
-            int inc = v[i];
-#pragma unroll
-            for (int s = 1; s < 32; s <<= 1) {
-                const int o = __shfl_up_sync(FULL_MASK, inc, s);
-                if (lane >= s) inc += o;
-            }
-            if (c < chunks) row[c] = run + inc - v[i];
-            run += __shfl_sync(FULL_MASK, inc, 31);
-        }
-    }
-    if (lane == 0) totals[e] = run;
-}
+__device__ __forceinline__ int redux_add(int v) { return __reduce_add_sync(FULL_MASK, v); }
 
-// WARPS warps take `per` consecutive slots each.  before / totals: NULL for the one CTA
-// that has all slots (both come from its own counts).
-template <int WARPS>
-__global__ void __launch_bounds__(32 * WARPS) plan_place_kernel(const int32_t* __restrict__ ids, int64_t n, int per,
-                                                                int E, const int32_t* __restrict__ before,
-                                                                const int32_t* __restrict__ totals,
+// A warp takes `per` consecutive slots.  counts: NULL for the one CTA that has all slots.
+__global__ void __launch_bounds__(32 * PL_WARPS) plan_place_kernel(const int32_t* __restrict__ ids, int64_t n, int per,
+                                                                int E, const int32_t* __restrict__ counts,
                                                                 int32_t* __restrict__ offs, int32_t* __restrict__ rows,
                                                                 int32_t* __restrict__ src) {
-    extern __shared__ int plan_s[];  // [WARPS][E] counts, then starts; [E] expert starts
+    extern __shared__ int plan_s[];  // [PL_WARPS][E] counts, then starts; [E] totals, then expert starts; [E] earlier;
+                                // [PL_WARPS][E] lanes of an expert
     __shared__ int routed_s;
     grid_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int* starts = plan_s + WARPS * E;
-    const int64_t first = ((int64_t)blockIdx.x * WARPS + warp) * per, end = min(n, first + per);
+    int* starts = plan_s + PL_WARPS * E;
+    int* before = starts + E;
     int* mine = plan_s + warp * E;
-    warp_count(ids, first, end, E, mine, lane);
-    __syncthreads();
-    // per expert: the warps' counts become starts relative to the expert's; its total
-    for (int e = threadIdx.x; e < E; e += 32 * WARPS) {
-        int run = before ? before[(int64_t)e * gridDim.x + blockIdx.x] : 0;
+    unsigned* mask = reinterpret_cast<unsigned*>(before + E) + warp * E;
+    const int64_t first = ((int64_t)blockIdx.x * PL_WARPS + warp) * per, end = min(n, first + per);
+    for (int e = lane; e < E; e += 32) mine[e] = 0, mask[e] = 0;
+    __syncwarp();
+    count_slots(ids, first, end, E, mine, lane);
+    if (counts) {
+        const int chunks = gridDim.x;
+        constexpr int L = (PL_MAX_CHUNKS + 31) / 32, B = 4;  // B experts' counts in flight
+        for (int e0 = warp; e0 < E; e0 += B * PL_WARPS) {
+            int v[B][L];
 #pragma unroll
-        for (int w = 0; w < WARPS; ++w) {
+            for (int i = 0; i < B; ++i)
+#pragma unroll
+                for (int j = 0; j < L; ++j) {
+                    const int e = e0 + i * PL_WARPS, c = 32 * j + lane;
+                    v[i][j] = e < E && c < chunks ? __ldg(counts + (int64_t)e * chunks + c) : 0;
+                }
+#pragma unroll
+            for (int i = 0; i < B; ++i) {
+                int all = 0, early = 0;
+#pragma unroll
+                for (int j = 0; j < L; ++j) {
+                    all += v[i][j];
+                    early += 32 * j + lane < (int)blockIdx.x ? v[i][j] : 0;
+                }
+                all = redux_add(all);
+                early = redux_add(early);
+                const int e = e0 + i * PL_WARPS;
+                if (lane == 0 && e < E) {
+                    starts[e] = all;
+                    before[e] = early;
+                }
+            }
+        }
+    }
+    __syncthreads();
+    // per expert: the warps' counts become starts relative to the expert's
+    for (int e = threadIdx.x; e < E; e += 32 * PL_WARPS) {
+        int run = counts ? before[e] : 0;
+#pragma unroll
+        for (int w = 0; w < PL_WARPS; ++w) {
             const int v = plan_s[w * E + e];
             plan_s[w * E + e] = run;
             run += v;
         }
-        starts[e] = totals ? totals[e] : run;
+        if (!counts) starts[e] = run;
     }
     __syncthreads();
     if (warp == 0) {  // exclusive prefix sum of the totals
@@ -145,55 +156,71 @@ __global__ void __launch_bounds__(32 * WARPS) plan_place_kernel(const int32_t* _
     }
     __syncthreads();
     const int routed = routed_s;
-#pragma unroll 4
-    for (int64_t a = first; a < end; a += 32) {
-        const int64_t at = a + lane;
-        const int id = slot_id(ids, at, end, E);
-        const unsigned same = __match_any_sync(FULL_MASK, id);
-        int r = -1;
-        if (id >= 0) r = starts[id] + mine[id] + __popc(same & ((1u << lane) - 1u));
-        __syncwarp();
-        if (id >= 0 && lane == __ffs(same) - 1) mine[id] += __popc(same);
-        __syncwarp();
-        if (at < end) {
-            rows[at] = r;
-            if (r >= 0) src[r] = (int32_t)at;
-            if (at >= routed) src[at] = -1;  // rows behind the last group
+    for (int64_t a = first; a < end; a += 32 * PL_BATCH) {
+        int ids_[PL_BATCH];
+        load_batch(ids, a, end, E, lane, ids_);
+#pragma unroll
+        for (int i = 0; i < PL_BATCH; ++i) {
+            const int64_t at = a + 32 * i + lane;
+            const int id = ids_[i];
+            if (id >= 0) atomicOr(mask + id, 1u << lane);
+            __syncwarp();
+            int r = -1, base = 0;
+            unsigned same = 0;
+            if (id >= 0) {
+                same = mask[id];
+                base = mine[id];
+                r = starts[id] + base + __popc(same & ((1u << lane) - 1u));
+            }
+            __syncwarp();
+            if (id >= 0 && lane == __ffs(same) - 1) {
+                mask[id] = 0;
+                mine[id] = base + __popc(same);
+            }
+            __syncwarp();
+            if (at < end) {
+                rows[at] = r;
+                if (r >= 0) src[r] = (int32_t)at;
+                if (at >= routed) src[at] = -1;  // rows behind the last group
+            }
         }
     }
 }
 
-int64_t plan_chunks(int64_t n) { return (n + PL_CHUNK - 1) / PL_CHUNK; }
+// Slots per warp and chunks of n > PL_ONE slots.
+struct PlanShape {
+    int per, chunks;
+};
+PlanShape plan_shape(int64_t n) {
+    const int64_t warps = (int64_t)PL_MAX_CHUNKS * PL_WARPS;
+    const int64_t per = std::max<int64_t>(PL_MIN_PER, ((n + warps - 1) / warps + 31) / 32 * 32);
+    return {(int)per, (int)((n + per * PL_WARPS - 1) / (per * PL_WARPS))};
+}
 
 }  // namespace
 
 // The one CTA needs none: its counts never leave it.
-int64_t plan_workspace_bytes(int64_t n, int E) { return n <= PL_ONE ? 0 : 4 * (plan_chunks(n) + 1) * E; }
+int64_t plan_workspace_bytes(int64_t n, int E) { return n <= PL_ONE ? 0 : 4 * (int64_t)plan_shape(n).chunks * E; }
 
 cudaError_t launch_moe_plan(const int32_t* ids, int64_t n, int E, int32_t* offs, int32_t* rows, int32_t* src,
                             int32_t* ws, cudaStream_t stream) {
-    if (n <= PL_ONE) {
-        // a slot per lane and step, at least one step for each warp
-        const size_t smem = (size_t)(PL_ONE_WARPS + 1) * E * sizeof(int);
-        const int per = std::max(32, (int)((n + 32 * PL_ONE_WARPS - 1) / (32 * PL_ONE_WARPS)) * 32);
-        const auto kernel = plan_place_kernel<PL_ONE_WARPS>;
-        if (smem > 48 * 1024) {
-            const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-            if (e != cudaSuccess) return e;
-        }
-        return launch_dependent(kernel, 1, 32 * PL_ONE_WARPS, smem, stream, ids, n, per, E, nullptr, nullptr, offs,
-                                rows, src);
+    const size_t smem = (size_t)(2 * PL_WARPS + 2) * E * sizeof(int);  // at most 136 KB
+    if (smem > 48 * 1024) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(plan_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
     }
-    const int chunks = (int)plan_chunks(n);
-    const size_t smem = (size_t)(PL_CHUNK_WARPS + 1) * E * sizeof(int);
-    int32_t* totals = ws + (int64_t)chunks * E;
-    cudaError_t e = launch_dependent(plan_count_kernel, chunks, 32 * PL_CHUNK_WARPS, smem, stream, ids, n, E, ws);
-    if (e == cudaSuccess)
-        e = launch_dependent(plan_scan_kernel, (E + 3) / 4, 128, 0, stream, ws, chunks, E, totals);
-    if (e == cudaSuccess)
-        e = launch_dependent(plan_place_kernel<PL_CHUNK_WARPS>, chunks, 32 * PL_CHUNK_WARPS, smem, stream, ids, n,
-                             PL_CHUNK / PL_CHUNK_WARPS, E, ws, totals, offs, rows, src);
-    return e;
+    if (n <= PL_ONE) {
+        const int per = std::max(32, (int)((n + 32 * PL_WARPS - 1) / (32 * PL_WARPS)) * 32);
+        return launch_dependent(plan_place_kernel, 1, 32 * PL_WARPS, smem, stream, ids, n, per, E, nullptr, offs, rows,
+                                src);
+    }
+    const PlanShape sh = plan_shape(n);
+    const cudaError_t e = launch_dependent(plan_count_kernel, sh.chunks, 32 * PL_WARPS, (size_t)E * sizeof(int),
+                                           stream, ids, n, sh.per, E, ws);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(plan_place_kernel, sh.chunks, 32 * PL_WARPS, smem, stream, ids, n, sh.per, E,
+                            ws, offs, rows, src);
 }
 
 }  // namespace mxq

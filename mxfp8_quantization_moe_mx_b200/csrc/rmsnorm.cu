@@ -76,16 +76,26 @@ __device__ __forceinline__ uint4 add8(const uint4& a, const uint4& b) {
     return make_uint4(add_bf16x2(a.x, b.x), add_bf16x2(a.y, b.y), add_bf16x2(a.z, b.z), add_bf16x2(a.w, b.w));
 }
 
-// Eight consecutive weights: four pairs as fp32.
-__device__ __forceinline__ void load_w8(const float* w, f2 (&f)[4]) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(w)), b = __ldg(reinterpret_cast<const float4*>(w) + 1);
-    f[0] = {a.x, a.y}, f[1] = {a.z, a.w}, f[2] = {b.x, b.y}, f[3] = {b.z, b.w};
-}
-__device__ __forceinline__ void load_w8(const uint16_t* w, f2 (&f)[4]) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(w));
-    f[0] = bf2(v.x), f[1] = bf2(v.y), f[2] = bf2(v.z), f[3] = bf2(v.w);
-}
-
+// Eight consecutive weights as they are stored, and as four pairs of fp32.
+template <typename W>
+struct W8;
+template <>
+struct W8<uint16_t> {
+    uint4 v;
+    __device__ __forceinline__ void load(const uint16_t* w) { v = __ldg(reinterpret_cast<const uint4*>(w)); }
+    __device__ __forceinline__ f2 pair(int j) const { return bf2(word(v, j)); }
+};
+template <>
+struct W8<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float* w) {
+        a = __ldg(reinterpret_cast<const float4*>(w));
+        b = __ldg(reinterpret_cast<const float4*>(w) + 1);
+    }
+    __device__ __forceinline__ f2 pair(int j) const {
+        return j == 0 ? f2{a.x, a.y} : j == 1 ? f2{a.z, a.w} : j == 2 ? f2{b.x, b.y} : f2{b.z, b.w};
+    }
+};
 // The thread's i-th vector of its V.
 template <int V>
 __device__ __forceinline__ int vec_of(int i) {
@@ -166,19 +176,17 @@ __device__ __forceinline__ void ring_leave(Ring* ring, int stages, int st, uint3
 
 // One row's norm and codes from its packed sums h[] (V vectors per thread), stored.
 template <int V, typename W>
-__device__ __forceinline__ void norm_row(const uint4 (&h)[V], const W* __restrict__ w, float r, int64_t at, int nv,
+__device__ __forceinline__ void norm_row(const uint4 (&h)[V], const W8<W> (&w)[V], float r, int64_t at, int nv,
                                          uint16_t* y, uint8_t* __restrict__ q, uint8_t* __restrict__ s) {
     const int lane = threadIdx.x & 31;
     uint32_t mine = 0;  // lane l < 8 V: the scale of the warp's block l
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int v = vec_of<V>(i);
-        f2 g[4] = {};
-        if (v < nv) load_w8(w + 8 * v, g);
         uint32_t p[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const f2 f = mul2(mul2(bf2(word(h[i], j)), f2{r, r}), g[j]);
+            const f2 f = mul2(mul2(bf2(word(h[i], j)), f2{r, r}), w[i].pair(j));
             p[j] = cvt_bf16x2(f.x, f.y);
         }
         const uint4 o = make_uint4(p[0], p[1], p[2], p[3]);
@@ -232,6 +240,10 @@ __global__ void __launch_bounds__(1024) rmsnorm_mx_few_kernel(const uint16_t* x,
     const int nv = D / 8;
     const int64_t m = blockIdx.x, at = m * D;
     uint4 h[V];
+    W8<W> g[V] = {};
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        if (vec_of<V>(i) < nv) g[i].load(w + 8 * vec_of<V>(i));
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int v = vec_of<V>(i);
@@ -247,12 +259,15 @@ __global__ void __launch_bounds__(1024) rmsnorm_mx_few_kernel(const uint16_t* x,
     }
     const float r = __frsqrt_rn(cta_sum(sum_squares<V>(h), part, 0) / (float)D + eps);
     if (rstd && threadIdx.x == 0) rstd[m] = r;
-    norm_row<V, W>(h, w, r, at, nv, y, q, s);
+    norm_row<V, W>(h, g, r, at, nv, y, q, s);
 }
 
 // Many rows.  V 8-element vectors per thread; D / 8 <= V * blockDim.x; RES: with a residual.
+// Held to 64 registers for five CTAs of 160 threads (D = 5120) on an SM.  65536 x 5120 with a
+// residual: 395 us, 5.97 TB/s, 91% of a copy (four CTAs at 88 registers 406 us; two vectors
+// per thread 410; the weights read again for every row, after its reduction, 416).
 template <int V, typename W, bool RES>
-__global__ void __launch_bounds__(512) rmsnorm_mx_kernel(const uint16_t* x, const uint16_t* residual,
+__global__ void __launch_bounds__(512, 2) rmsnorm_mx_kernel(const uint16_t* x, const uint16_t* residual,
                                                          const W* __restrict__ w, int64_t M, int D, float eps,
                                                          uint16_t* res_out, uint16_t* y, uint8_t* __restrict__ q,
                                                          uint8_t* __restrict__ s, float* __restrict__ rstd,
@@ -265,6 +280,10 @@ __global__ void __launch_bounds__(512) rmsnorm_mx_kernel(const uint16_t* x, cons
     const int tid = threadIdx.x, nv = D / 8;
     const uint16_t* const from[3] = {x, residual, nullptr};
     ring_start<N>(norm_sm, &ring, stages, from, M, D);
+    W8<W> g[V] = {};
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        if (vec_of<V>(i) < nv) g[i].load(w + 8 * vec_of<V>(i));
     int st = 0, turn = 0;
     uint32_t phase = 0;
     for (int64_t m = blockIdx.x; m < M; m += gridDim.x, turn ^= 1) {
@@ -300,7 +319,7 @@ __global__ void __launch_bounds__(512) rmsnorm_mx_kernel(const uint16_t* x, cons
         }
         const float r = __frsqrt_rn(sum / (float)D + eps);
         if (rstd && tid == 0) rstd[m] = r;
-        norm_row<V, W>(h, w, r, at, nv, y, q, s);
+        norm_row<V, W>(h, g, r, at, nv, y, q, s);
     }
 }
 
@@ -310,6 +329,8 @@ __global__ void __launch_bounds__(512) rmsnorm_mx_kernel(const uint16_t* x, cons
 // A CTA walks rows blockIdx.x, + gridDim.x, ... and keeps its share of gw in registers
 // (fp32), writes it to its row of the workspace, and a second kernel adds the CTAs' rows in
 // order: no atomics, the same bits every time.
+// 16640 x 5120 with a residual's gradient: 104 us, 6.5 TB/s (the weights read again for every
+// row: 127 us; without the ring: 227).
 template <int V, typename W, bool RES>
 __global__ void __launch_bounds__(512) rmsnorm_backward_kernel(
     const uint16_t* gy, const uint16_t* __restrict__ h, const W* __restrict__ w, const float* __restrict__ rstd,
@@ -322,6 +343,10 @@ __global__ void __launch_bounds__(512) rmsnorm_backward_kernel(
     const int tid = threadIdx.x, nv = D / 8;
     const uint16_t* const from[3] = {gy, h, gres};
     ring_start<N>(norm_sm, &ring, stages, from, M, D);
+    W8<W> g[V] = {};
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        if (vec_of<V>(i) < nv) g[i].load(w + 8 * vec_of<V>(i));
     f2 gw[V][4] = {};
     int st = 0, turn = 0;
     uint32_t phase = 0;
@@ -340,13 +365,11 @@ __global__ void __launch_bounds__(512) rmsnorm_backward_kernel(
             a[i] = lds_v4(row + 16 * v);
             b[i] = lds_v4(row + 2 * D + 16 * v);
             if (RES) e[i] = lds_v4(row + 4 * D + 16 * v);
-            f2 g[4];
-            load_w8(w + 8 * v, g);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const f2 f = bf2(word(a[i], j)), n = mul2(bf2(word(b[i], j)), f2{r, r});
                 gw[i][j] = fma2(f, n, gw[i][j]);
-                dot = fma2(mul2(f, g[j]), n, dot);
+                dot = fma2(mul2(f, g[i].pair(j)), n, dot);
             }
         }
         const float mean = cta_sum(dot.x + dot.y, part, turn, true) / (float)D;  // with a barrier: the stage is read
@@ -366,13 +389,11 @@ __global__ void __launch_bounds__(512) rmsnorm_backward_kernel(
         for (int i = 0; i < V; ++i) {
             const int v = vec_of<V>(i);
             if (v >= nv) continue;
-            f2 g[4];
-            load_w8(w + 8 * v, g);
             uint32_t o[4];
             const float k = -r * r * mean;  // r (f g - n mean) = f g r - h r^2 mean
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                f2 t = mul2(mul2(bf2(word(a[i], j)), g[j]), f2{r, r});
+                f2 t = mul2(mul2(bf2(word(a[i], j)), g[i].pair(j)), f2{r, r});
                 t = fma2(bf2(word(b[i], j)), f2{k, k}, t);
                 if (RES) t = fma2(bf2(word(e[i], j)), f2{1.0f, 1.0f}, t);
                 o[j] = cvt_bf16x2(t.x, t.y);
