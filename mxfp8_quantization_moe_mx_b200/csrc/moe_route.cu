@@ -331,28 +331,55 @@ __device__ __forceinline__ void extract(float (&c)[NI], int n, int lane, int& id
     }
 }
 
-// The same for n <= 16, by a threshold.  The n-th largest of the lanes' own maxima is at most
-// the row's n-th best candidate, so the candidates from it up are all that can be chosen:
-// about -32 ln(1 - n / 32) of them for values in no order (9 for n = 8, 22 for n = 16).  They
-// are gathered in index order, and each counts the ones before it.  False, with nothing
-// done, where more than 32 are left (rows of equal logits).
-struct Picked {
-    float val[33];
-    int id[33];
+// The exact value of candidate e, in 64 bits: score + bias (max and sum: softmax's, over the
+// row in 64 bits).
+__device__ __forceinline__ double exact_candidate(float l, float b, int score, double max, double sum) {
+    double p, q;
+    if (score == 1)
+        sigmoid_pair<double>((double)l, p, q);
+    else
+        p = exp((double)l - max) / sum;
+    return p + (double)b;
+}
+
+// Softmax's sum over the row in 64 bits, to every lane.
+template <int NI, typename L>
+__device__ __noinline__ double exact_sum(const L* row, int E, double max, int lane) {
+    double s = 0.0;
+#pragma unroll 1
+    for (int e = lane; e < E; e += 32) s += exp((double)ld_logit(row + e) - max);
+    return warp_sum(s);
+}
+
+// The k <= 16 best by a threshold.  The k-th largest of the lanes' own maxima is at most the
+// row's k-th best candidate, so the candidates from it up (`slack` lower, where a candidate
+// may be that far from its exact value) are all that can be chosen: about -32 ln(1 - k / 32)
+// of them for values in no order (9 for k = 8, 22 for k = 16).  They are gathered in index
+// order, and each counts the ones before it.  With a bias, candidates closer together than
+// their errors are counted again by their values in 64 bits.  Lane j < k gets the j-th id.
+// False, with nothing done, where more than 32 are left (rows of equal logits).
+struct __align__(16) Picked {
+    float val[36];  // 32, and one for what is not picked
+    float err[36];
+    int id[36];
 };
-template <int NI>
-__device__ __forceinline__ bool select_few(const float (&c)[NI], int n, int lane, Picked* s, int& id, float& val,
-                                           int& last_id, float& last_val) {
+// 1 if the value o of a candidate before (`earlier`) or after this one goes before v.
+__device__ __forceinline__ int before(float o, float v, bool earlier) { return o > v || (o == v && earlier); }
+
+template <int NI, typename L>
+__device__ __forceinline__ bool select_few(const float (&c)[NI], const RouteArgs& a, const L* row, float rel,
+                                           float slack, float top, int lane, Picked* s, int& id) {
     const float NEG = neg_inf<float>();
-    float head = c[0];
+    float h = c[0];
 #pragma unroll
-    for (int i = 1; i < NI; ++i) head = fmaxf(head, c[i]);
-    float t = NEG, h = head;
-    for (int j = 0; j < n; ++j) {  // equal maxima leave together: the threshold only gets lower
+    for (int i = 1; i < NI; ++i) h = fmaxf(h, c[i]);
+    float t = NEG;
+    for (int j = 0; j < a.k; ++j) {  // equal maxima leave together: the threshold only gets lower
         t = redux_max(h);
         if (h == t) h = NEG;
     }
-    const float low = t > NEG ? t : -3.402823466e38f;  // fewer lanes than n have any: all finite ones
+    // fewer lanes than k have any: all finite ones
+    const float low = t > NEG ? fmaxf(t - slack, -3.402823466e38f) : -3.402823466e38f;
     int mine = 0;
 #pragma unroll
     for (int i = 0; i < NI; ++i) mine += c[i] >= low;
@@ -366,36 +393,59 @@ __device__ __forceinline__ bool select_few(const float (&c)[NI], int n, int lane
     if (cnt > 32) return false;
     pos -= mine;
 #pragma unroll
-    for (int i = 0; i < NI; ++i)
-        if (c[i] >= low) {
-            s->val[pos] = c[i];
-            s->id[pos++] = lane * NI + i;
-        }
+    for (int i = 0; i < NI; ++i) {  // without branches: the others go to a place of their own
+        const bool in = c[i] >= low;
+        const int at = in ? pos : 32;
+        s->val[at] = c[i];
+        s->id[at] = lane * NI + i;
+        pos += in;
+    }
     __syncwarp();
-    float v = NEG;
+    float v = NEG, err = 0.0f, b = 0.0f;
     int e = -1, rank = 0;
     if (lane < cnt) {
         v = s->val[lane];
         e = s->id[lane];
     }
-    for (int j = 0; j < cnt; ++j) {
-        const float o = __shfl_sync(FULL_MASK, v, j);
-        rank += o > v || (o == v && j < lane);
+    if (a.bias) {
+        if (lane < cnt) {
+            b = __ldg(a.bias + e);
+            err = cand_err(rel, fabsf(v - b), v);
+        }
+        s->val[lane] = v;  // the places behind the last hold -inf
+        s->err[lane] = err;
+        __syncwarp();
+        int near = 0;  // candidates that this one may tie with, itself among them
+        for (int j = 0; j < cnt; j += 4) {
+            const float4 o = *reinterpret_cast<const float4*>(s->val + j), f = *reinterpret_cast<const float4*>(s->err + j);
+            rank += before(o.x, v, j < lane) + before(o.y, v, j + 1 < lane) + before(o.z, v, j + 2 < lane) +
+                    before(o.w, v, j + 3 < lane);
+            // (not of equal infinite ones, which tie by index: their difference is no number)
+            near += (fabsf(o.x - v) <= err + f.x) + (fabsf(o.y - v) <= err + f.y) + (fabsf(o.z - v) <= err + f.z) +
+                    (fabsf(o.w - v) <= err + f.w);
+        }
+        if (__any_sync(FULL_MASK, near > 1)) {
+            const double sum = a.score == 0 ? exact_sum<NI, L>(row, a.E, (double)top, lane) : 1.0;
+            const double x = lane < cnt ? exact_candidate(ld_logit(row + e), b, a.score, (double)top, sum) : 0.0;
+            rank = 0;
+            for (int j = 0; j < cnt; ++j) {
+                const double o = __shfl_sync(FULL_MASK, x, j);
+                rank += o > x || (o == x && j < lane);
+            }
+        }
+    } else {
+        s->val[lane] = v;
+        __syncwarp();
+        for (int j = 0; j < cnt; j += 4) {
+            const float4 o = *reinterpret_cast<const float4*>(s->val + j);
+            rank += before(o.x, v, j < lane) + before(o.y, v, j + 1 < lane) + before(o.z, v, j + 2 < lane) +
+                    before(o.w, v, j + 3 < lane);
+        }
     }
     __syncwarp();
-    if (lane < cnt) {
-        s->val[rank] = v;
-        s->id[rank] = e;
-    }
+    if (lane < cnt) s->id[rank] = e;
     __syncwarp();
-    id = -1;
-    val = NEG;
-    if (lane < min(cnt, n)) {
-        val = s->val[lane];
-        id = s->id[lane];
-    }
-    last_id = cnt >= n ? s->id[n - 1] : -1;
-    last_val = cnt >= n ? s->val[n - 1] : NEG;
+    id = lane < min(cnt, a.k) ? s->id[lane] : -1;
     __syncwarp();
     return true;
 }
@@ -420,6 +470,7 @@ __global__ void __launch_bounds__(32 * RT_WARPS, NI <= 8 ? 4 : NI <= 16 ? 2 : 1)
                                                                   int32_t* __restrict__ ids) {
     extern __shared__ double route_rows[];
     __shared__ Picked picked[RT_WARPS];
+    grid_wait();
     const float NEG = neg_inf<float>(), INF = __int_as_float(0x7F800000);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t n_warps = (int64_t)gridDim.x * RT_WARPS;
@@ -429,12 +480,22 @@ __global__ void __launch_bounds__(32 * RT_WARPS, NI <= 8 ? 4 : NI <= 16 ? 2 : 1)
     const bool need_p = have_bias || by_p;
     const int gs = a.E / a.n_groups, gl = gs / NI;  // elements and lanes of a group
     const bool runs = gl > 0 && gl * NI == gs && (gl & (gl - 1)) == 0;
+    const int gl_log = 31 - __clz(gl > 0 ? gl : 1);
     float* row_s = reinterpret_cast<float*>(route_rows + (int64_t)warp * a.E);
     constexpr bool KEEP_BIAS = NI <= 8;  // the lane's biases stay in registers
     float bias[KEEP_BIAS ? NI : 1];
     if (KEEP_BIAS)
 #pragma unroll
         for (int i = 0; i < NI; ++i) bias[i] = have_bias && lane * NI + i < a.E ? __ldg(a.bias + lane * NI + i) : 0.0f;
+    // the largest finite bias, for the roundings of the candidates
+    float bias_mag = 0.0f;
+    if (have_bias) {
+        for (int e = lane; e < a.E; e += 32) {
+            const float b = fabsf(__ldg(a.bias + e));
+            if (b < INF) bias_mag = fmaxf(bias_mag, b);
+        }
+        bias_mag = redux_max(bias_mag);
+    }
     for (int64_t t = (int64_t)blockIdx.x * RT_WARPS + warp; t < a.T; t += n_warps) {
         const L* row = logits + t * a.E;
         float l[NI], c[NI];
@@ -507,7 +568,7 @@ __global__ void __launch_bounds__(32 * RT_WARPS, NI <= 8 ? 4 : NI <= 16 ? 2 : 1)
                     second = fmaxf(fmaxf(second, os), fminf(best, ob));
                     best = fmaxf(best, ob);
                 }
-                g0 = lane / gl;
+                g0 = lane >> gl_log;
             } else {
                 // any other shape: lane g scans group g in shared memory
 #pragma unroll
@@ -523,34 +584,32 @@ __global__ void __launch_bounds__(32 * RT_WARPS, NI <= 8 ? 4 : NI <= 16 ? 2 : 1)
                 __syncwarp();
                 g0 = lane;
             }
-            const int step = runs ? gl : 1;  // lane of group g: g * step
-            const bool in = g0 < a.n_groups;
-            const bool some = in && best > NEG;
-            float gsum = best;
-            if (a.group_top == 2 && some && second > NEG) gsum = best + second;
-            int before = 0;
-            for (int h = 0; h < a.n_groups; ++h) {
-                const float o = __shfl_sync(FULL_MASK, gsum, h * step);
-                if (o > gsum || (o == gsum && h < g0)) ++before;
+            const bool some = g0 < a.n_groups && best > NEG;
+            float gsum = NEG;
+            if (some) gsum = a.group_top == 2 && second > NEG ? best + second : best;
+            // the best group at a time, equal ones in order; every lane of a group has its sum
+            float h = gsum, lo = NEG;
+            kept = false;
+            for (int j = 0; j < a.top_groups; ++j) {
+                const float m = redux_max(h);
+                if (!(m > NEG)) break;
+                lo = m;
+                const int win = __ffs(__ballot_sync(FULL_MASK, h == m)) - 1;
+                if (g0 == (runs ? win >> gl_log : win)) {
+                    kept = true;
+                    h = NEG;
+                }
             }
-            kept = some && before < a.top_groups;
             if (need_p) {
                 // the border: the worst kept group against the best one left out.  Each sum has
                 // at most two candidates' errors and one addition's; with a bias the scores are
                 // bounded by 1 and the roundings by the candidates' magnitudes
-                const float lo = -redux_max(kept ? -gsum : NEG);
-                const float hi = redux_max(some && !kept ? gsum : NEG);
-                if (hi > NEG && lo < INF) {
+                const float hi = redux_max(h);
+                if (hi > NEG) {
                     const float rel = a.score == 1 ? RT_REL_SIGMOID : RT_REL;
-                    float err = (lo + hi) * (2.0f * rel) + 0x1p-120f;
-                    if (!by_p) {
-                        const float mag =
-                            redux_max(some ? fabsf(best) + (second > NEG ? fabsf(second) : 0.0f) : 0.0f);
-                        err = 4.0f * rel + mag * 0x1p-21f;
-                    }
-                    sure = lo - hi > err;
-                } else if (hi > NEG) {
-                    sure = false;  // infinite sums on both sides
+                    const float err = by_p ? (lo + hi) * (2.0f * rel) + 0x1p-120f
+                                           : 4.0f * rel + (bias_mag + 1.0f) * 0x1p-19f;
+                    sure = lo - hi > err;  // false where both are infinite
                 }
             }
             if (runs) {
@@ -566,32 +625,36 @@ __global__ void __launch_bounds__(32 * RT_WARPS, NI <= 8 ? 4 : NI <= 16 ? 2 : 1)
                 }
             }
         }
-        // the k best; with a bias one more, to see that the order is beyond doubt
-        int id = -1, last_id = -1;
-        float val = NEG, last_val = NEG;
+        int id = -1;
         if (sure) {
-            const int n = have_bias ? a.k + 1 : a.k;
-            if (n > 16 || !select_few<NI>(c, n, lane, &picked[warp], id, val, last_id, last_val))
-                extract<NI>(c, n, lane, id, val, last_id, last_val);
-            if (lane >= a.k) id = -1;
-            if (have_bias) {
-                // each against the next one: lane j has the j-th, every lane the last
-                const float lj = id >= 0 ? ld_logit(row + id) : 0.0f, bj = id >= 0 ? __ldg(a.bias + id) : 0.0f;
-                const float rel = a.score == 1 ? RT_REL_SIGMOID : RT_REL;
-                const float err = cand_err(rel, fabsf(val - bj), val);
-                int nid = __shfl_down_sync(FULL_MASK, id, 1);
-                float nv = __shfl_down_sync(FULL_MASK, val, 1), nl = __shfl_down_sync(FULL_MASK, lj, 1),
-                      nb = __shfl_down_sync(FULL_MASK, bj, 1), ne = __shfl_down_sync(FULL_MASK, err, 1);
-                if (lane == a.k - 1) {
-                    nid = last_id;
-                    nv = last_val;
-                    nl = nid >= 0 ? ld_logit(row + nid) : 0.0f;
-                    nb = nid >= 0 ? __ldg(a.bias + nid) : 0.0f;
-                    ne = cand_err(rel, fabsf(nv - nb), nv);
+            const float rel = a.score == 1 ? RT_REL_SIGMOID : RT_REL;
+            // scores are at most 1, so no finite candidate is further than half of this from
+            // its exact value
+            const float slack = have_bias ? 2.0f * rel + (bias_mag + 1.0f) * 0x1p-20f : 0.0f;
+            if (a.k > 16 || !select_few<NI, L>(c, a, row, rel, slack, top, lane, &picked[warp], id)) {
+                // with a bias one more than k, to see that the order is beyond doubt
+                int last_id = -1;
+                float val = NEG, last_val = NEG;
+                extract<NI>(c, have_bias ? a.k + 1 : a.k, lane, id, val, last_id, last_val);
+                if (lane >= a.k) id = -1;
+                if (have_bias) {
+                    // each against the next one: lane j has the j-th, every lane the last
+                    const float lj = id >= 0 ? ld_logit(row + id) : 0.0f, bj = id >= 0 ? __ldg(a.bias + id) : 0.0f;
+                    const float err = cand_err(rel, fabsf(val - bj), val);
+                    int nid = __shfl_down_sync(FULL_MASK, id, 1);
+                    float nv = __shfl_down_sync(FULL_MASK, val, 1), nl = __shfl_down_sync(FULL_MASK, lj, 1),
+                          nb = __shfl_down_sync(FULL_MASK, bj, 1), ne = __shfl_down_sync(FULL_MASK, err, 1);
+                    if (lane == a.k - 1) {
+                        nid = last_id;
+                        nv = last_val;
+                        nl = nid >= 0 ? ld_logit(row + nid) : 0.0f;
+                        nb = nid >= 0 ? __ldg(a.bias + nid) : 0.0f;
+                        ne = cand_err(rel, fabsf(nv - nb), nv);
+                    }
+                    const bool close = id >= 0 && nid >= 0 && !(val - nv > err + ne) && !(lj == nl && bj == nb) &&
+                                       fabsf(val) < INF;  // infinite candidates tie by index, exactly
+                    sure = !__any_sync(FULL_MASK, close);
                 }
-                const bool close = id >= 0 && nid >= 0 && !(val - nv > err + ne) && !(lj == nl && bj == nb) &&
-                                   fabsf(val) < INF;  // infinite candidates tie by index, exactly
-                sure = !__any_sync(FULL_MASK, close);
             }
         }
         if (!sure) id = choose_exact<NI, L>(row, a, route_rows + (int64_t)warp * a.E, lane);
@@ -679,6 +742,7 @@ __global__ void __launch_bounds__(32 * RT_WARPS) moe_route_backward_kernel(
     // a row per warp: the lanes' values lie with a stride of NI + 1, so that they meet in
     // different banks
     __shared__ float grad_rows[RT_WARPS][32 * (NI + 1)];
+    grid_wait();
     const float NEG = neg_inf<float>();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     float* row_s = grad_rows[warp];
@@ -736,13 +800,17 @@ __global__ void __launch_bounds__(32 * RT_WARPS) moe_route_backward_kernel(
                 d = r * (g - warp_sum(g * r));
             }
         }
+        // whether an index comes twice: each slot leaves its number at its expert
+        const int at = mine ? id / NI * (NI + 1) + id % NI : 0;
+        if (mine) row_s[at] = (float)lane;
+        __syncwarp();
+        const bool twice = __any_sync(FULL_MASK, mine && row_s[at] != (float)lane);
+        __syncwarp();
 #pragma unroll
         for (int i = 0; i < NI; ++i) row_s[lane * (NI + 1) + i] = base[i];
         __syncwarp();
         // the chosen entries; an index that comes twice is added in the order of its slots
-        const int at = mine ? id / NI * (NI + 1) + id % NI : 0;
-        const unsigned same = __match_any_sync(FULL_MASK, mine ? id : -1 - lane);
-        if (__any_sync(FULL_MASK, (same & (same - 1)) != 0)) {
+        if (twice) {
             for (int j = 0; j < a.k; ++j) {
                 if (lane == j && mine) row_s[at] += d;
                 __syncwarp();
@@ -771,32 +839,28 @@ cudaError_t by_width(int E, F&& f) {
 
 }  // namespace
 
+// Several CTAs' rows per resident CTA, so that rows of unlike cost even out.
+static unsigned route_grid(int64_t T) {
+    return (unsigned)std::min<int64_t>((T + RT_WARPS - 1) / RT_WARPS, (int64_t)sm_count() * 16);
+}
+
 cudaError_t launch_moe_route(const void* logits, bool bf16, int64_t T, int E, const float* bias, int score,
                              int n_groups, int top_groups, int group_top, int k, bool renorm, float scale,
                              float* weights, int32_t* ids, cudaStream_t stream) {
     const RouteArgs a{bias, T, E, k, n_groups, top_groups, group_top, score, renorm ? 1 : 0, scale};
-    const int64_t ctas = (T + RT_WARPS - 1) / RT_WARPS;
-    const unsigned grid = (unsigned)std::min<int64_t>(ctas, (int64_t)sm_count() * 8);
     const size_t smem = n_groups > 1 ? (size_t)RT_WARPS * E * sizeof(double) : 0;  // a row per warp, for the groups
     return by_width(E, [&](auto ni) {
         constexpr int NI = decltype(ni)::value;
-        cudaError_t e = cudaSuccess;
-        if (bf16) {
-            if (smem > 48 * 1024)
-                e = cudaFuncSetAttribute(moe_route_kernel<NI, uint16_t>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem);
-            if (e != cudaSuccess) return e;
-            moe_route_kernel<NI, uint16_t><<<grid, 32 * RT_WARPS, smem, stream>>>(
-                static_cast<const uint16_t*>(logits), a, weights, ids);
-        } else {
-            if (smem > 48 * 1024)
-                e = cudaFuncSetAttribute(moe_route_kernel<NI, float>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem);
-            if (e != cudaSuccess) return e;
-            moe_route_kernel<NI, float><<<grid, 32 * RT_WARPS, smem, stream>>>(static_cast<const float*>(logits), a,
-                                                                               weights, ids);
-        }
-        return cudaGetLastError();
+        auto go = [&](auto kernel, auto l) {
+            if (smem > 46 * 1024) {
+                const cudaError_t e =
+                    cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+                if (e != cudaSuccess) return e;
+            }
+            return launch_dependent(kernel, route_grid(T), 32 * RT_WARPS, smem, stream, l, a, weights, ids);
+        };
+        return bf16 ? go(moe_route_kernel<NI, uint16_t>, static_cast<const uint16_t*>(logits))
+                    : go(moe_route_kernel<NI, float>, static_cast<const float*>(logits));
     });
 }
 
@@ -804,17 +868,14 @@ cudaError_t launch_moe_route_backward(const void* logits, bool bf16, int64_t T, 
                                       const float* grad_weights, int score, bool renorm, float scale,
                                       void* grad_logits, cudaStream_t stream) {
     const RouteArgs a{nullptr, T, E, k, 1, 1, 1, score, renorm ? 1 : 0, scale};
-    const int64_t ctas = (T + RT_WARPS - 1) / RT_WARPS;
-    const unsigned grid = (unsigned)std::min<int64_t>(ctas, (int64_t)sm_count() * 8);
     return by_width(E, [&](auto ni) {
         constexpr int NI = decltype(ni)::value;
-        if (bf16)
-            moe_route_backward_kernel<NI, uint16_t><<<grid, 32 * RT_WARPS, 0, stream>>>(
-                static_cast<const uint16_t*>(logits), a, ids, grad_weights, static_cast<uint16_t*>(grad_logits));
-        else
-            moe_route_backward_kernel<NI, float><<<grid, 32 * RT_WARPS, 0, stream>>>(
-                static_cast<const float*>(logits), a, ids, grad_weights, static_cast<float*>(grad_logits));
-        return cudaGetLastError();
+        return bf16 ? launch_dependent(moe_route_backward_kernel<NI, uint16_t>, route_grid(T), 32 * RT_WARPS, 0, stream,
+                                       static_cast<const uint16_t*>(logits), a, ids, grad_weights,
+                                       static_cast<uint16_t*>(grad_logits))
+                    : launch_dependent(moe_route_backward_kernel<NI, float>, route_grid(T), 32 * RT_WARPS, 0, stream,
+                                       static_cast<const float*>(logits), a, ids, grad_weights,
+                                       static_cast<float*>(grad_logits));
     });
 }
 
