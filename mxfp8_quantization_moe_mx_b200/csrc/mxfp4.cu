@@ -70,6 +70,7 @@ __device__ __forceinline__ uint32_t block_amax(const uint4& v) {
 template <int U>
 __global__ void __launch_bounds__(256) f4_quant_kernel(const uint16_t* __restrict__ x, uint8_t* __restrict__ q,
                                                         uint8_t* __restrict__ s, int64_t n_blocks) {
+    grid_wait();
     const int lane = threadIdx.x & 31, part = lane & 3, sub = lane >> 2;
     const int64_t gwarp = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
     const int64_t n_warps = (int64_t)gridDim.x * (blockDim.x >> 5);
@@ -108,6 +109,7 @@ __global__ void __launch_bounds__(256, 5) f4_quant_blocked_kernel(const uint16_t
                                                                int64_t tiles_per_matrix) {
     __shared__ __align__(16) uint8_t sc[128][16];
     __shared__ int64_t info[2];  // first source row of the tile, valid rows in it (-1: no tile)
+    grid_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t tile = blockIdx.x;
     if (G <= 0) {
@@ -233,6 +235,7 @@ __device__ __forceinline__ uint4 f4_dequant8(uint32_t codes, uint32_t b) {
 template <int U>
 __global__ void __launch_bounds__(256) f4_dequant_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ s,
                                                          uint16_t* __restrict__ y, int64_t n8) {
+    grid_wait();
     const int lane = threadIdx.x & 31;
     const int64_t gwarp = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5), n_warps = (int64_t)gridDim.x * 8;
     for (int64_t base = gwarp * (32 * U); base < n8; base += n_warps * (32 * U)) {
@@ -259,26 +262,24 @@ cudaError_t launch_f4_quant(const uint16_t* x, int64_t batch, int64_t rows, int6
         constexpr int U = 4;
         const int64_t n_blocks = batch * rows * (cols / 32);
         const int64_t ctas = (n_blocks + 8 * 8 * U - 1) / (8 * 8 * U);
-        f4_quant_kernel<U><<<(unsigned)std::min<int64_t>(ctas, (int64_t)sm_count() * 8), 256, 0, stream>>>(x, q, s,
-                                                                                                         n_blocks);
-        return cudaGetLastError();
+        return launch_dependent(f4_quant_kernel<U>, (unsigned)std::min<int64_t>(ctas, (int64_t)sm_count() * 8), 256, 0,
+                                stream, x, q, s, n_blocks);
     }
     const int64_t per = (rows + 127) / 128;
     const int64_t tiles = G > 0 ? (rows + 127 * (int64_t)G) / 128 : batch * per;
     const int64_t chunks = (cols + 511) / 512;
     if (tiles > 0x7FFFFFFFLL || chunks > 65535) return cudaErrorInvalidConfiguration;
-    if (tiles > 0 && chunks > 0)
-        f4_quant_blocked_kernel<<<dim3((unsigned)tiles, (unsigned)chunks), 256, 0, stream>>>(x, rows, cols, q, s, sf,
-                                                                                             offs, G, per);
-    return cudaGetLastError();
+    if (tiles <= 0 || chunks <= 0) return cudaSuccess;
+    return launch_dependent(f4_quant_blocked_kernel, dim3((unsigned)tiles, (unsigned)chunks), 256, 0, stream, x, rows,
+                            cols, q, s, sf, offs, G, per);
 }
 
 cudaError_t launch_f4_dequant(const uint8_t* q, const uint8_t* s, uint16_t* y, int64_t n, cudaStream_t stream) {
     constexpr int U = 4;
     const int64_t n8 = n / 8;
     const int64_t ctas = (n8 + 256 * U - 1) / (256 * U);
-    f4_dequant_kernel<U><<<(unsigned)std::min<int64_t>(ctas, (int64_t)sm_count() * 8), 256, 0, stream>>>(q, s, y, n8);
-    return cudaGetLastError();
+    return launch_dependent(f4_dequant_kernel<U>, (unsigned)std::min<int64_t>(ctas, (int64_t)sm_count() * 8), 256, 0,
+                            stream, q, s, y, n8);
 }
 
 }  // namespace mxq

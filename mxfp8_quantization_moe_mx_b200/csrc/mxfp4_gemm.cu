@@ -127,24 +127,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1) f4_gemm_wide
     const int64_t n_tiles_n = N / FW_BN;
     const int64_t col_tiles = K / 128;
 
+    if (warp == 0 && lane == 0) {
+        abort_s = 0;
+        issued_s[0] = issued_s[1] = 0;
+        for (int s = 0; s < FW_STAGES; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        mbar_init(&acc_full, 1);
+        mbar_init(&acc_empty, 8);  // the epilogue warps of both CTAs
+        mbar_init(&drained, 1);
+    }
+    if (warp == 1) tmem_alloc_pair(&tmem_base_s, 512);
+    grid_wait();  // the operands and offsets are the work of earlier kernels
     if (warp == 0) {
         PairTile pt;
         int64_t total;
         gg_find_pair(offs, G, M, -1, &pt, &total);
-        if (lane == 0) {
-            n_work_s = total * n_tiles_n;
-            abort_s = 0;
-            issued_s[0] = issued_s[1] = 0;
-            for (int s = 0; s < FW_STAGES; ++s) {
-                mbar_init(&full[s], 1);
-                mbar_init(&empty[s], 1);
-            }
-            mbar_init(&acc_full, 1);
-            mbar_init(&acc_empty, 8);  // the epilogue warps of both CTAs
-            mbar_init(&drained, 1);
-        }
+        if (lane == 0) n_work_s = total * n_tiles_n;
     }
-    if (warp == 1) tmem_alloc_pair(&tmem_base_s, 512);
     tc_fence_before();
     cluster_sync();  // both CTAs' barriers are initialised before either signals the other's
     tc_fence_after();
@@ -449,27 +450,28 @@ __global__ void __launch_bounds__(192, 1) f4_gemm_narrow_kernel(
     const int64_t n_w = N / F4_ROWS;  // weight tiles of a group
     const int64_t col_tiles = K / 128;
 
-    if (warp == 0) {
-        const int n = fill_table(offs, G, M, &tab);
-        if (lane == 0) {
-            n_tiles_s = n;
-            abort_s = 0;
-            for (int s = 0; s < S; ++s) {
-                mbar_init(&full[s], 1);
-                mbar_init(&empty[s], 1);
-            }
-            for (int s = 0; s < 2; ++s) {
-                mbar_init(&acc_full[s], 1);
-                mbar_init(&acc_empty[s], 4);
-            }
-            mbar_init(&drained, 1);
+    if (warp == 0 && lane == 0) {
+        abort_s = 0;
+        for (int s = 0; s < S; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
         }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&acc_full[s], 1);
+            mbar_init(&acc_empty[s], 4);
+        }
+        mbar_init(&drained, 1);
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                          smem_addr(&tmem_base_s))
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    grid_wait();  // the operands and offsets are the work of earlier kernels
+    if (warp == 0) {
+        const int n = fill_table(offs, G, M, &tab);
+        if (lane == 0) n_tiles_s = n;
     }
     tc_fence_before();
     __syncthreads();
@@ -641,8 +643,8 @@ cudaError_t launch_narrow(const uint8_t* qa, const uint8_t* sfa, const uint8_t* 
     if (e != cudaSuccess) return e;
     const int64_t units = std::min((M + 127 * (int64_t)G) / 128, M) * (N / F4_ROWS);  // an upper bound
     const unsigned grid = (unsigned)std::min<int64_t>(units, sm_count());
-    f4_gemm_narrow_kernel<<<grid, 192, FN_SMEM, stream>>>(m.b, m.a, a8, m.sfb, m.sfa, offs, G, M, N, K, out);
-    return cudaGetLastError();
+    return launch_dependent(f4_gemm_narrow_kernel, grid, 192, FN_SMEM, stream, m.b, m.a, a8, m.sfb, m.sfa, offs, G, M,
+                            N, K, out);
 }
 
 }  // namespace
@@ -673,9 +675,8 @@ cudaError_t launch_mxfp4_grouped_gemm(const uint8_t* qa, const uint8_t* sfa, con
     if (e != cudaSuccess) return e;
     const int64_t units = (m_tiles + G) / 2 * (N / FW_BN);
     const int64_t pairs = std::max<int64_t>(1, std::min<int64_t>(units, sm_count() / 2));
-    f4_gemm_wide_kernel<<<(unsigned)(2 * pairs), 192, FW_SMEM, stream>>>(m.a, m.b, m.sfa, m.sfb, offs, G, M, N, K,
-                                                                         out);
-    return cudaGetLastError();
+    return launch_dependent(f4_gemm_wide_kernel, (unsigned)(2 * pairs), 192, FW_SMEM, stream, m.a, m.b, m.sfa, m.sfb,
+                            offs, G, M, N, K, out);
 }
 
 }  // namespace mxq
