@@ -367,6 +367,12 @@ def _run(f, dev: int, stream, *args) -> None:
         _check(status)
 
 
+def _tiles_bytes(batch: int, rows: int, n_k: int, G: int) -> int:
+    """mx_scales_blocked_bytes, for sizes that the call itself checks."""
+    tiles = (rows + 127 * G) // 128 if G else batch * ((rows + 127) // 128)
+    return tiles * ((n_k + 3) // 4) * 512
+
+
 def _two(t: torch.Tensor, name: str, what: str) -> tuple[int, int]:
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
         raise MxqError(f"{name} must be {what}")
@@ -474,7 +480,7 @@ def mxfp4_quantize(x: torch.Tensor, q: torch.Tensor, s: torch.Tensor | None = No
     size = 0
     if sf_blocked is not None:
         size = sf_blocked.numel()
-        if size < mx_scales_blocked_bytes(batch, rows, cols // 32, G):
+        if size < _tiles_bytes(batch, rows, cols // 32, G):
             raise MxqError("sf_blocked is smaller than mx_scales_blocked_bytes")
     elif s is None:
         raise MxqError("mxfp4_quantize needs s or sf_blocked for the scales")
@@ -507,9 +513,9 @@ def mxfp4_grouped_gemm(qa: torch.Tensor, sfa_blocked: torch.Tensor, qb: torch.Te
         raise MxqError("qa, qb and offs disagree on K or G")
     K, dev, u8 = 2 * Kb, _first(qa, "qa"), torch.uint8
     na, nb = sfa_blocked.numel(), sfb_blocked.numel()
-    if na < mx_scales_blocked_bytes(1, M, K // 32, G):
+    if na < _tiles_bytes(1, M, K // 32, G):
         raise MxqError("sfa_blocked is smaller than mx_scales_blocked_bytes(1, M, K/32, G)")
-    if nb < mx_scales_blocked_bytes(G, N, K // 32, 0):
+    if nb < _tiles_bytes(G, N, K // 32, 0):
         raise MxqError("sfb_blocked is smaller than mx_scales_blocked_bytes(G, N, K/32, 0)")
     _run(lib().mxfp4_grouped_gemm, dev, stream, _arg(qa, u8, "qa", M * Kb, dev),
          _arg(sfa_blocked, u8, "sfa_blocked", na, dev), _arg(qb, u8, "qb", G * N * Kb, dev),

@@ -168,3 +168,14 @@ def test_binding_refuses_host_and_wrong_tensors(L):
         mxq.moe_plan_workspace_bytes(-1, 4)
     with pytest.raises(mxq.MxqError):
         mxq.rmsnorm_backward_workspace_bytes(4, 20)
+
+
+def test_the_layer_forms_refuse_host_and_misshapen_tensors(L):
+    from mxfp8_quantization_moe_mx_b200 import moe
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    for call in (lambda: moe.route(x, 2), lambda: moe.route(x[0], 2), lambda: moe.plan(torch.zeros(4, dtype=torch.int32), 2),
+                 lambda: moe.rmsnorm(x, x[0].float()), lambda: moe.rmsnorm(x, x[0], residual=x[:2]),
+                 lambda: moe.rmsnorm(x[0], x[0]), lambda: moe.Mxfp4Experts(x),
+                 lambda: moe.Mxfp4Experts(torch.zeros(2, 256, 128, dtype=torch.bfloat16))):
+        with pytest.raises(mxq.MxqError):
+            call()
