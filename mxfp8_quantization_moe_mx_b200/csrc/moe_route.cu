@@ -90,6 +90,7 @@ struct RouteArgs {
     int64_t T;
     int E, k, n_groups, top_groups, group_top, score, renorm;
     float scale;
+    int gs, gl_log;  // experts of a group; log2 of its lanes where a group is a run of whole lanes, else -1
 };
 
 // Scores of the lane's elements (softmax over the whole row, or sigmoid); masked (-inf)
@@ -121,17 +122,21 @@ __device__ __forceinline__ void scores(const float (&l)[NI], int score, R (&p)[N
     for (int i = 0; i < NI; ++i) p[i] *= inv;
 }
 
-// How far the 32-bit value of a candidate c = p + b may be from the exact one.  Relative
-// error of a softmax score: l - max rounded (|l - max| 2^-24 <= 104 * 2^-24 before the score
-// is zero in 32 bits), exp within 2 units in the last place, the sum of up to 1024 terms in
-// chains of 32 + 5 additions, two roundings more: together under 2^-16.  Of a sigmoid:
-// the argument is exact; exp, one addition, a reciprocal and a product: under 2^-20.  Then
-// the addition's rounding, and the underflow of scores below 2^-126.
-constexpr float RT_REL = 0x1p-16f, RT_REL_SIGMOID = 0x1p-20f;
-__device__ __forceinline__ float cand_err(float rel, float p, float c) {
+// How far the 32-bit value of a candidate c = p + b may be from the exact one.
+// A softmax score's relative error: l - max rounded (|l - max| 2^-24 <= 104 * 2^-24 before the
+// score is zero in 32 bits), exp within 2 units in the last place, the sum of up to 1024 terms
+// in chains of 32 + 5 additions, two roundings more: together under 2^-16.
+// A sigmoid's: u = __expf(-|l|) is within 2 + 1.173 |l| units in the last place, 124 at
+// |l| = 104, with an addition, a reciprocal and a product more under 2^-16 relative; since
+// dp = p (1 - p) du / u, and p (1 - p) (2 + 1.173 |l|) < 0.65, under 2^-21 absolute.
+// Then the addition's rounding, and the underflow of scores below 2^-126.
+constexpr float RT_REL = 0x1p-16f, RT_ABS_SIGMOID = 0x1p-21f;
+__device__ __forceinline__ float cand_err(int score, float p, float c) {
     // p comes as c - b, itself rounded
-    return p * rel + fabsf(c) * 0x1p-22f + 0x1p-126f;
+    return (score == 1 ? RT_ABS_SIGMOID : p * RT_REL) + fabsf(c) * 0x1p-22f + 0x1p-126f;
 }
+// The largest of any score: scores are at most 1.
+__device__ __forceinline__ float score_err(int score) { return score == 1 ? RT_ABS_SIGMOID : RT_REL; }
 
 // The choice in 64 bits: lane j < k gets the id of the j-th (-1 if there are fewer).  The
 // lane holds the elements lane + 32 i; `sc` is the warp's shared row of E values.
@@ -154,7 +159,7 @@ __device__ __forceinline__ void choose_in_64(const float (&l)[NI], const RouteAr
             if (e < a.E) sc[e] = by_p && c[i] != NEG ? p[i] : c[i];
         }
         __syncwarp();
-        const int gs = a.E / a.n_groups;
+        const int gs = a.gs;
         double best = NEG, second = NEG;
         if (lane < a.n_groups)
             for (int j = 0; j < gs; ++j) {
@@ -367,8 +372,8 @@ struct __align__(16) Picked {
 __device__ __forceinline__ int before(float o, float v, bool earlier) { return o > v || (o == v && earlier); }
 
 template <int NI, typename L>
-__device__ __forceinline__ bool select_few(const float (&c)[NI], const RouteArgs& a, const L* row, float rel,
-                                           float slack, float top, int lane, Picked* s, int& id) {
+__device__ __forceinline__ bool select_few(const float (&c)[NI], const RouteArgs& a, const L* row, float slack,
+                                           float top, int lane, Picked* s, int& id) {
     const float NEG = neg_inf<float>();
     float h = c[0];
 #pragma unroll
@@ -410,7 +415,7 @@ __device__ __forceinline__ bool select_few(const float (&c)[NI], const RouteArgs
     if (a.bias) {
         if (lane < cnt) {
             b = __ldg(a.bias + e);
-            err = cand_err(rel, fabsf(v - b), v);
+            err = cand_err(a.score, fabsf(v - b), v);
         }
         s->val[lane] = v;  // the places behind the last hold -inf
         s->err[lane] = err;
@@ -478,9 +483,8 @@ __global__ void __launch_bounds__(32 * RT_WARPS, NI <= 8 ? 4 : NI <= 16 ? 2 : 1)
     const bool have_bias = a.bias != nullptr, grouped = a.n_groups > 1;
     const bool by_p = grouped && !have_bias && a.group_top == 2;  // groups by scores, candidates logits
     const bool need_p = have_bias || by_p;
-    const int gs = a.E / a.n_groups, gl = gs / NI;  // elements and lanes of a group
-    const bool runs = gl > 0 && gl * NI == gs && (gl & (gl - 1)) == 0;
-    const int gl_log = 31 - __clz(gl > 0 ? gl : 1);
+    const int gs = a.gs, gl_log = a.gl_log, gl = 1 << (gl_log < 0 ? 0 : gl_log);
+    const bool runs = gl_log >= 0;
     float* row_s = reinterpret_cast<float*>(route_rows + (int64_t)warp * a.E);
     constexpr bool KEEP_BIAS = NI <= 8;  // the lane's biases stay in registers
     float bias[KEEP_BIAS ? NI : 1];
@@ -513,7 +517,7 @@ __global__ void __launch_bounds__(32 * RT_WARPS, NI <= 8 ? 4 : NI <= 16 ? 2 : 1)
             if (a.score == 1) {
 #pragma unroll
                 for (int i = 0; i < NI; ++i) {
-                    const float u = expf(-fabsf(l[i])), inv = rcp1(1.0f + u);
+                    const float u = __expf(-fabsf(l[i])), inv = rcp1(1.0f + u);
                     p[i] = l[i] < 0.0f ? u * inv : inv;  // 0 for -inf
                 }
             } else {
@@ -606,9 +610,8 @@ __global__ void __launch_bounds__(32 * RT_WARPS, NI <= 8 ? 4 : NI <= 16 ? 2 : 1)
                 // bounded by 1 and the roundings by the candidates' magnitudes
                 const float hi = redux_max(h);
                 if (hi > NEG) {
-                    const float rel = a.score == 1 ? RT_REL_SIGMOID : RT_REL;
-                    const float err = by_p ? (lo + hi) * (2.0f * rel) + 0x1p-120f
-                                           : 4.0f * rel + (bias_mag + 1.0f) * 0x1p-19f;
+                    const float err = by_p ? (lo + hi) * (2.0f * RT_REL) + 0x1p-120f
+                                           : 4.0f * score_err(a.score) + (bias_mag + 1.0f) * 0x1p-19f;
                     sure = lo - hi > err;  // false where both are infinite
                 }
             }
@@ -627,11 +630,9 @@ __global__ void __launch_bounds__(32 * RT_WARPS, NI <= 8 ? 4 : NI <= 16 ? 2 : 1)
         }
         int id = -1;
         if (sure) {
-            const float rel = a.score == 1 ? RT_REL_SIGMOID : RT_REL;
-            // scores are at most 1, so no finite candidate is further than half of this from
-            // its exact value
-            const float slack = have_bias ? 2.0f * rel + (bias_mag + 1.0f) * 0x1p-20f : 0.0f;
-            if (a.k > 16 || !select_few<NI, L>(c, a, row, rel, slack, top, lane, &picked[warp], id)) {
+            // no finite candidate is further than half of this from its exact value
+            const float slack = have_bias ? 2.0f * score_err(a.score) + (bias_mag + 1.0f) * 0x1p-20f : 0.0f;
+            if (a.k > 16 || !select_few<NI, L>(c, a, row, slack, top, lane, &picked[warp], id)) {
                 // with a bias one more than k, to see that the order is beyond doubt
                 int last_id = -1;
                 float val = NEG, last_val = NEG;
@@ -640,7 +641,7 @@ __global__ void __launch_bounds__(32 * RT_WARPS, NI <= 8 ? 4 : NI <= 16 ? 2 : 1)
                 if (have_bias) {
                     // each against the next one: lane j has the j-th, every lane the last
                     const float lj = id >= 0 ? ld_logit(row + id) : 0.0f, bj = id >= 0 ? __ldg(a.bias + id) : 0.0f;
-                    const float err = cand_err(rel, fabsf(val - bj), val);
+                    const float err = cand_err(a.score, fabsf(val - bj), val);
                     int nid = __shfl_down_sync(FULL_MASK, id, 1);
                     float nv = __shfl_down_sync(FULL_MASK, val, 1), nl = __shfl_down_sync(FULL_MASK, lj, 1),
                           nb = __shfl_down_sync(FULL_MASK, bj, 1), ne = __shfl_down_sync(FULL_MASK, err, 1);
@@ -649,7 +650,7 @@ __global__ void __launch_bounds__(32 * RT_WARPS, NI <= 8 ? 4 : NI <= 16 ? 2 : 1)
                         nv = last_val;
                         nl = nid >= 0 ? ld_logit(row + nid) : 0.0f;
                         nb = nid >= 0 ? __ldg(a.bias + nid) : 0.0f;
-                        ne = cand_err(rel, fabsf(nv - nb), nv);
+                        ne = cand_err(a.score, fabsf(nv - nb), nv);
                     }
                     const bool close = id >= 0 && nid >= 0 && !(val - nv > err + ne) && !(lj == nl && bj == nb) &&
                                        fabsf(val) < INF;  // infinite candidates tie by index, exactly
@@ -847,10 +848,12 @@ static unsigned route_grid(int64_t T) {
 cudaError_t launch_moe_route(const void* logits, bool bf16, int64_t T, int E, const float* bias, int score,
                              int n_groups, int top_groups, int group_top, int k, bool renorm, float scale,
                              float* weights, int32_t* ids, cudaStream_t stream) {
-    const RouteArgs a{bias, T, E, k, n_groups, top_groups, group_top, score, renorm ? 1 : 0, scale};
+    RouteArgs a{bias, T, E, k, n_groups, top_groups, group_top, score, renorm ? 1 : 0, scale, E / n_groups, -1};
     const size_t smem = n_groups > 1 ? (size_t)RT_WARPS * E * sizeof(double) : 0;  // a row per warp, for the groups
     return by_width(E, [&](auto ni) {
         constexpr int NI = decltype(ni)::value;
+        for (int log = 0; log < 6; ++log)
+            if (a.gs == NI << log) a.gl_log = log;
         auto go = [&](auto kernel, auto l) {
             if (smem > 46 * 1024) {
                 const cudaError_t e =
@@ -867,7 +870,7 @@ cudaError_t launch_moe_route(const void* logits, bool bf16, int64_t T, int E, co
 cudaError_t launch_moe_route_backward(const void* logits, bool bf16, int64_t T, int E, const int32_t* ids, int k,
                                       const float* grad_weights, int score, bool renorm, float scale,
                                       void* grad_logits, cudaStream_t stream) {
-    const RouteArgs a{nullptr, T, E, k, 1, 1, 1, score, renorm ? 1 : 0, scale};
+    const RouteArgs a{nullptr, T, E, k, 1, 1, 1, score, renorm ? 1 : 0, scale, E, -1};
     return by_width(E, [&](auto ni) {
         constexpr int NI = decltype(ni)::value;
         return bf16 ? launch_dependent(moe_route_backward_kernel<NI, uint16_t>, route_grid(T), 32 * RT_WARPS, 0, stream,
