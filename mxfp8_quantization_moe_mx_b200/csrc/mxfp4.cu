@@ -106,12 +106,13 @@ __global__ void __launch_bounds__(256, 5) f4_quant_blocked_kernel(const uint16_t
                                                                int64_t cols, uint8_t* __restrict__ q,
                                                                uint8_t* __restrict__ s, uint8_t* __restrict__ sf,
                                                                const int32_t* __restrict__ offs, int32_t G,
-                                                               int64_t tiles_per_matrix) {
+                                                               int64_t tiles_per_matrix, int chunks) {
     __shared__ __align__(16) uint8_t sc[128][16];
     __shared__ int64_t info[2];  // first source row of the tile, valid rows in it (-1: no tile)
     grid_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t tile = blockIdx.x;
+    const int64_t tile = blockIdx.x / (unsigned)chunks;  // a tile's chunks side by side
+    const int chunk = (int)(blockIdx.x % (unsigned)chunks);
     if (G <= 0) {
         if (tid == 0) {
             const int64_t b = tile / tiles_per_matrix, i = tile % tiles_per_matrix;
@@ -158,7 +159,7 @@ __global__ void __launch_bounds__(256, 5) f4_quant_blocked_kernel(const uint16_t
     __syncthreads();
     const int64_t r0 = info[0], valid = info[1];
     if (valid < 0) return;
-    const int64_t c0 = (int64_t)blockIdx.y * 512;
+    const int64_t c0 = (int64_t)chunk * 512;
     const int64_t n_k = cols / 32;
     constexpr int R = 2;  // rows of a warp in flight
     for (int rr = warp; rr < valid; rr += 8 * R) {
@@ -192,7 +193,7 @@ __global__ void __launch_bounds__(256, 5) f4_quant_blocked_kernel(const uint16_t
     if (tid < 128) {
         const int64_t col_tiles = (n_k + 3) / 4;
         const int j = tid >> 5;  // scale tile of this CTA's four
-        const int64_t ct = (int64_t)blockIdx.y * 4 + j;
+        const int64_t ct = (int64_t)chunk * 4 + j;
         if (ct < col_tiles) {
             uint32_t w[4];
 #pragma unroll
@@ -268,10 +269,10 @@ cudaError_t launch_f4_quant(const uint16_t* x, int64_t batch, int64_t rows, int6
     const int64_t per = (rows + 127) / 128;
     const int64_t tiles = G > 0 ? (rows + 127 * (int64_t)G) / 128 : batch * per;
     const int64_t chunks = (cols + 511) / 512;
-    if (tiles > 0x7FFFFFFFLL || chunks > 65535) return cudaErrorInvalidConfiguration;
     if (tiles <= 0 || chunks <= 0) return cudaSuccess;
-    return launch_dependent(f4_quant_blocked_kernel, dim3((unsigned)tiles, (unsigned)chunks), 256, 0, stream, x, rows,
-                            cols, q, s, sf, offs, G, per);
+    if (tiles > 0x7FFFFFFFLL / chunks) return cudaErrorInvalidConfiguration;
+    return launch_dependent(f4_quant_blocked_kernel, (unsigned)(tiles * chunks), 256, 0, stream, x, rows, cols, q, s,
+                            sf, offs, G, per, (int)chunks);
 }
 
 cudaError_t launch_f4_dequant(const uint8_t* q, const uint8_t* s, uint16_t* y, int64_t n, cudaStream_t stream) {
