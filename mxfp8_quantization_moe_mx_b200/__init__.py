@@ -336,9 +336,13 @@ def _opt(t, dtype, name: str, numel: int, dev: int):
 
 def _first(t: torch.Tensor, name: str) -> int:
     """The device of a call: that of its first tensor."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    try:
+        dev = t.get_device()
+    except AttributeError:
+        dev = -1
+    if dev < 0:
         raise MxqError(f"{name} must be a CUDA tensor")
-    return t.get_device()
+    return dev
 
 
 def _type_of(t, name: str) -> int:
@@ -374,9 +378,11 @@ def _tiles_bytes(batch: int, rows: int, n_k: int, G: int) -> int:
 
 
 def _two(t: torch.Tensor, name: str, what: str) -> tuple[int, int]:
-    if not isinstance(t, torch.Tensor) or t.dim() != 2:
-        raise MxqError(f"{name} must be {what}")
-    return t.shape[0], t.shape[1]
+    try:
+        rows, cols = t.shape
+    except (AttributeError, ValueError):
+        raise MxqError(f"{name} must be {what}") from None
+    return rows, cols
 
 
 def moe_route(logits: torch.Tensor, weights: torch.Tensor, ids: torch.Tensor, bias: torch.Tensor | None = None,
