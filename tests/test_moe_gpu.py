@@ -569,20 +569,22 @@ def test_fp4_product_of_some_rows(M, N, K, sizes):
 
 @pytest.mark.parametrize("M,N,K,sizes", [
     (256, 256, 256, [256]),
-    (320, 256, 128, [200, 120]),                     # half a stage
-    (1024, 512, 640, [129, 1, 257, 383, 230]),       # ragged, odd numbers of tiles
-    (700, 256, 1920, [650, 40]),                     # more stages than the ring
-    (1037, 256, 256, [300, 0, 700]),                 # rows behind the last group
+    (320, 256, 128, [200, 120]),
+    # enough units for the 256 x 256 tiles (more than one wave of the 128 x 128 ones)
+    (256, 9984, 128, [256]),                         # half a stage
+    (1024, 2560, 640, [129, 1, 257, 383, 230]),      # ragged, odd numbers of tiles
+    (700, 4096, 1920, [650, 40]),                    # more stages than the ring
+    (1037, 2560, 256, [300, 0, 700]),                # rows behind the last group
 ])
 def test_fp4_product_of_many_rows(M, N, K, sizes):
     check_product(M, N, K, np.cumsum(sizes), seed=M + K)
 
 
-@pytest.mark.parametrize("M,G", [(20, 3), (200, 3), (800, 3)])
-def test_fp4_product_offsets_and_nan(M, G):
-    check_product(M, 256, 640, [M // 3, M // 4, 5 * M], seed=M, special=True)   # decreasing, then past the end
-    check_product(M, 256, 384, [-7, 0, M // 2], seed=M, special=True)
-    check_product(M, 256, 256, [0, 0, 0], seed=M)
+@pytest.mark.parametrize("M,N", [(20, 256), (200, 256), (800, 256), (800, 2560)])
+def test_fp4_product_offsets_and_nan(M, N):
+    check_product(M, N, 640, [M // 3, M // 4, 5 * M], seed=M, special=True)   # decreasing, then past the end
+    check_product(M, N, 384, [-7, 0, M // 2], seed=M, special=True)
+    check_product(M, N, 256, [0, 0, 0], seed=M)
 
 
 def test_fp4_product_more_units_than_processors():
@@ -594,10 +596,11 @@ def test_fp4_product_more_units_than_processors():
 
 
 def test_fp4_product_many_groups():
-    """More groups than the table in shared memory holds."""
-    sizes = np.zeros(1100, int)
-    sizes[[0, 3, 700, 1050, 1099]] = [2, 1, 130, 5, 9]
-    check_product(int(sizes.sum()), 256, 128, np.cumsum(sizes))
+    """More groups than the table in shared memory holds, and as many."""
+    for G in (1100, 1024):
+        sizes = np.zeros(G, int)
+        sizes[[0, 3, 700, 1010, G - 1]] = [2, 1, 130, 5, 9]
+        check_product(int(sizes.sum()), 256, 128, np.cumsum(sizes))
 
 
 # ---- a layer ------------------------------------------------------------------------------------------------

@@ -143,7 +143,7 @@ def test_a_training_step_through_norm_router_and_experts():
     od = torch.einsum("td,tknd->tkn", yb, mats.double()[ids.long()])
     lossd = ((od * pr[:, :, None]).sum(1) ** 2).mean()
     lossd.backward()
-    assert abs(float(loss) - float(lossd)) <= 1e-5 * float(lossd)
+    assert abs(float(loss.detach()) - float(lossd.detach())) <= 1e-5 * float(lossd.detach())
     # fp32 products of 64 terms and the router's gradient: 2^-14 of the largest; x's gradient
     # passes bf16 once (gradient of y) and is rounded to it: 2^-7
     for a, b, tol in ((router.grad, routerd.grad, 2.0 ** -12), (w.grad, wd.grad, 2.0 ** -7), (x.grad, xd.grad, 2.0 ** -7)):
