@@ -261,7 +261,7 @@ enum { MXQ_SCORE_SOFTMAX = 0, MXQ_SCORE_SIGMOID = 1 };
 
 /*
  * moe_route -- the k experts of each token and their weights.
- *  logits  (T, E) of `type` (MXQ_TYPE_*), 16-byte aligned; 1 <= E <= 1024.
+ *  logits  (T, E) of `type` (MXQ_TYPE_*), aligned to their type; 1 <= E <= 1024.
  *  bias    (E) fp32 added to the scores for the choice alone (a balancing bias), or NULL.
  *  Scores p = softmax(logits) over the row, or sigmoid(logits).  Candidates c = p + bias;
  *  without a bias the logits themselves are compared (both functions are monotone).
@@ -292,8 +292,7 @@ int moe_route(const void* logits, int type, int64_t T, int64_t E, const float* b
  *  ids (T, k) as moe_route wrote them (entries outside 0 .. E-1 are skipped; an index that
  *  comes twice in a row counts twice), grad_weights (T, k) fp32; logits, score, renorm and
  *  scale as for moe_route.
- *  grad_logits (T, E) of the logits' type, 16-byte aligned, must not overlap them: written
- *  whole.  The choice itself has no gradient; the bias takes none.  Masked experts get 0;
+ *  grad_logits (T, E) of the logits' type, must not overlap them: written whole.  The choice itself has no gradient; the bias takes none.  Masked experts get 0;
  *  softmax's gradient reaches every expert of the row, unless renorm confines it to the
  *  chosen ones.
  *  Returns as moe_route.
@@ -310,7 +309,7 @@ int moe_route_backward(const void* logits, int type, int64_t T, int64_t E, const
  *        are [offs[e-1], offs[e]).
  *  rows  (n) the row of each slot, -1 where it has none.
  *  src   (n) the slot of each row, in the order of the slots within an expert; -1 for the
- *        rows at and past offs[E-1].
+ *        rows at and past offs[E-1].  None of the arrays may overlap another.
  *  workspace  moe_plan_workspace_bytes(n, E) bytes of device memory, 4-byte aligned (NULL
  *        where that is 0); calls that may run at the same time, and graphs captured from
  *        them, each need their own.
@@ -332,6 +331,8 @@ int64_t moe_plan_workspace_bytes(int64_t n, int64_t E);
  *  res_out (M, D) bf16 receives h (NULL: not written); it may be x or residual itself.
  *  y (M, D) bf16 and rstd (M) fp32 (r, for the backward pass) may be NULL.
  *  All (.., D) tensors 16-byte aligned.  Apart from res_out nothing may overlap.
+ *  With many rows the kernels here wait, bounded (2 s), for copies into shared memory; a CTA
+ *  that gives up leaves its remaining rows unwritten and is counted by mxq_wait_timeouts.
  *  Returns MXQ_OK, MXQ_ERR_ARG (a type, eps), MXQ_ERR_SHAPE, MXQ_ERR_NULL, MXQ_ERR_ALIGN
  *  or MXQ_ERR_CUDA.
  */

@@ -233,7 +233,8 @@ int moe_route(const void* logits, int type, int64_t T, int64_t E, const float* b
     if (!route_shape_ok(T, E, k) || E % n_groups != 0) return MXQ_ERR_SHAPE;
     if (T == 0) return MXQ_OK;
     if (!logits || !weights || !ids) return MXQ_ERR_NULL;
-    if (!aligned(logits, 16) || !aligned(bias, 4) || !aligned(weights, 4) || !aligned(ids, 4)) return MXQ_ERR_ALIGN;
+    if (!aligned(logits, type == MXQ_TYPE_BF16 ? 2 : 4) || !aligned(bias, 4) || !aligned(weights, 4) || !aligned(ids, 4))
+        return MXQ_ERR_ALIGN;
     return cuda_status(mxq::launch_moe_route(logits, type == MXQ_TYPE_BF16, T, (int)E, bias, score, n_groups,
                                              top_groups, group_top, k, renorm != 0, scale, weights, ids,
                                              as_stream(stream)));
@@ -246,7 +247,8 @@ int moe_route_backward(const void* logits, int type, int64_t T, int64_t E, const
     if (!route_shape_ok(T, E, k)) return MXQ_ERR_SHAPE;
     if (T == 0) return MXQ_OK;
     if (!logits || !ids || !grad_weights || !grad_logits) return MXQ_ERR_NULL;
-    if (!aligned(logits, 16) || !aligned(ids, 4) || !aligned(grad_weights, 4) || !aligned(grad_logits, 16))
+    const uintptr_t size = type == MXQ_TYPE_BF16 ? 2 : 4;
+    if (!aligned(logits, size) || !aligned(ids, 4) || !aligned(grad_weights, 4) || !aligned(grad_logits, size))
         return MXQ_ERR_ALIGN;
     return cuda_status(mxq::launch_moe_route_backward(logits, type == MXQ_TYPE_BF16, T, (int)E, ids, k, grad_weights,
                                                       score, renorm != 0, scale, grad_logits, as_stream(stream)));

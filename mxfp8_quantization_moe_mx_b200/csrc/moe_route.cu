@@ -91,6 +91,7 @@ struct RouteArgs {
     int E, k, n_groups, top_groups, group_top, score, renorm;
     float scale;
     int gs, gl_log;  // experts of a group; log2 of its lanes where a group is a run of whole lanes, else -1
+    bool aligned;    // the row arrays start on 16-byte boundaries
 };
 
 // Scores of the lane's elements (softmax over the whole row, or sigmoid); masked (-inf)
@@ -479,7 +480,7 @@ __global__ void __launch_bounds__(32 * RT_WARPS, NI <= 8 ? 4 : NI <= 16 ? 2 : 1)
     const float NEG = neg_inf<float>(), INF = __int_as_float(0x7F800000);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t n_warps = (int64_t)gridDim.x * RT_WARPS;
-    const bool vec = row_vec<NI, L>(a.E);
+    const bool vec = a.aligned && row_vec<NI, L>(a.E);
     const bool have_bias = a.bias != nullptr, grouped = a.n_groups > 1;
     const bool by_p = grouped && !have_bias && a.group_top == 2;  // groups by scores, candidates logits
     const bool need_p = have_bias || by_p;
@@ -747,7 +748,7 @@ __global__ void __launch_bounds__(32 * RT_WARPS) moe_route_backward_kernel(
     const float NEG = neg_inf<float>();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     float* row_s = grad_rows[warp];
-    const bool vec = row_vec<NI, L>(a.E);
+    const bool vec = a.aligned && row_vec<NI, L>(a.E);
     const int64_t n_warps = (int64_t)gridDim.x * RT_WARPS;
     for (int64_t t = (int64_t)blockIdx.x * RT_WARPS + warp; t < a.T; t += n_warps) {
         const L* row = logits + t * a.E;
@@ -840,6 +841,8 @@ cudaError_t by_width(int E, F&& f) {
 
 }  // namespace
 
+static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
 // Several CTAs' rows per resident CTA, so that rows of unlike cost even out.
 static unsigned route_grid(int64_t T) {
     return (unsigned)std::min<int64_t>((T + RT_WARPS - 1) / RT_WARPS, (int64_t)sm_count() * 16);
@@ -848,7 +851,8 @@ static unsigned route_grid(int64_t T) {
 cudaError_t launch_moe_route(const void* logits, bool bf16, int64_t T, int E, const float* bias, int score,
                              int n_groups, int top_groups, int group_top, int k, bool renorm, float scale,
                              float* weights, int32_t* ids, cudaStream_t stream) {
-    RouteArgs a{bias, T, E, k, n_groups, top_groups, group_top, score, renorm ? 1 : 0, scale, E / n_groups, -1};
+    RouteArgs a{bias, T, E, k, n_groups, top_groups, group_top, score, renorm ? 1 : 0, scale, E / n_groups, -1,
+                aligned16(logits)};
     const size_t smem = n_groups > 1 ? (size_t)RT_WARPS * E * sizeof(double) : 0;  // a row per warp, for the groups
     return by_width(E, [&](auto ni) {
         constexpr int NI = decltype(ni)::value;
@@ -870,7 +874,8 @@ cudaError_t launch_moe_route(const void* logits, bool bf16, int64_t T, int E, co
 cudaError_t launch_moe_route_backward(const void* logits, bool bf16, int64_t T, int E, const int32_t* ids, int k,
                                       const float* grad_weights, int score, bool renorm, float scale,
                                       void* grad_logits, cudaStream_t stream) {
-    const RouteArgs a{nullptr, T, E, k, 1, 1, 1, score, renorm ? 1 : 0, scale, E, -1};
+    const RouteArgs a{nullptr, T, E, k, 1, 1, 1, score, renorm ? 1 : 0, scale, E, -1,
+                      aligned16(logits) && aligned16(grad_logits)};
     return by_width(E, [&](auto ni) {
         constexpr int NI = decltype(ni)::value;
         return bf16 ? launch_dependent(moe_route_backward_kernel<NI, uint16_t>, route_grid(T), 32 * RT_WARPS, 0, stream,

@@ -138,8 +138,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1) f4_gemm_wide
         mbar_init(&acc_empty, 8);  // the epilogue warps of both CTAs
         mbar_init(&drained, 1);
     }
+    // The operands and offsets are the work of earlier kernels.  Tensor memory is taken after
+    // they have ended and before later ones may come: a kernel that waits for another holds
+    // none of it.
+    grid_depend_wait();
     if (warp == 1) tmem_alloc_pair(&tmem_base_s, 512);
-    grid_wait();  // the operands and offsets are the work of earlier kernels
     if (warp == 0) {
         PairTile pt;
         int64_t total;
@@ -149,6 +152,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1) f4_gemm_wide
     tc_fence_before();
     cluster_sync();  // both CTAs' barriers are initialised before either signals the other's
     tc_fence_after();
+    grid_release();
     const uint32_t tmem = tmem_base_s;
     const int64_t n_work = n_work_s;
     const uint32_t full0 = cluster_map(&full[0], 0);  // the first CTA's `full` ring (8 bytes apart)
@@ -462,13 +466,13 @@ __global__ void __launch_bounds__(192, 1) f4_gemm_narrow_kernel(
         }
         mbar_init(&drained, 1);
     }
+    grid_depend_wait();  // then tensor memory, as in the wide kernel
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                          smem_addr(&tmem_base_s))
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    grid_wait();  // the operands and offsets are the work of earlier kernels
     if (warp == 0) {
         const int n = fill_table(offs, G, M, &tab);
         if (lane == 0) n_tiles_s = n;
@@ -476,6 +480,7 @@ __global__ void __launch_bounds__(192, 1) f4_gemm_narrow_kernel(
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    grid_release();
     const uint32_t tmem = tmem_base_s;
     const int64_t n_work = n_tiles_s * n_w;
 

@@ -19,13 +19,17 @@ constexpr unsigned FULL_MASK = 0xFFFFFFFFu;
 // ---- programmatic dependent launch ---------------------------------------------------
 
 // Wait until the kernel before this one in the stream has ended and its writes are visible
-// (returns at once where the launch made no such dependence), then let the next kernel's
-// CTAs become resident as this one's leave room: it waits in its own grid_wait.  Every
-// kernel launched by launch_dependent begins with this, in every thread, before any access
-// to global memory.
+// (returns at once where the launch made no such dependence).  Every kernel launched by
+// launch_dependent does this, in every thread, before any access to global memory.
+__device__ __forceinline__ void grid_depend_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Let the next kernel's CTAs become resident as this one's leave room (they wait in their own
+// grid_depend_wait).
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 __device__ __forceinline__ void grid_wait() {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    grid_depend_wait();
+    grid_release();
 }
 
 // ---- loads / stores ----------------------------------------------------------------

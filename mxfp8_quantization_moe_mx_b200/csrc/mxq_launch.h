@@ -11,8 +11,8 @@ namespace mxq {
 int sm_count();
 
 // Launch with programmatic dependence on the kernel before it in the stream: the CTAs may
-// become resident before that kernel has ended, so `kernel` begins with grid_wait(), which
-// holds every thread until it has (and its writes are visible).
+// become resident before that kernel has ended, so `kernel` holds every thread in
+// grid_depend_wait() until it has (and its writes are visible) before it touches global memory.
 template <typename... P, typename... A>
 inline cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
                                     A&&... args) {

@@ -32,7 +32,7 @@ def test_moe_route_argument_errors(L):
         assert _route(L, **kw) == SHAPE, kw
     for kw in (dict(logits=None), dict(w=None), dict(i=None)):
         assert _route(L, **kw) == NULL, kw
-    for kw in (dict(logits=P8), dict(bias=P2), dict(w=P2), dict(i=P2)):
+    for kw in (dict(logits=P + 1), dict(logits=P2, ty=1), dict(bias=P2), dict(w=P2), dict(i=P2)):
         assert _route(L, **kw) == ALIGN, kw
     assert _route(L, T=0, logits=None, w=None, i=None) == OK
 
@@ -50,7 +50,8 @@ def test_moe_route_backward_argument_errors(L):
     assert go(a2=-1) == SHAPE and go(a3=2000) == SHAPE and go(a5=0) == SHAPE and go(a5=65) == SHAPE
     for i in (0, 4, 6, 10):
         assert go(**{f"a{i}": None}) == NULL
-    assert go(a0=P8) == ALIGN and go(a4=P2) == ALIGN and go(a6=P2) == ALIGN and go(a10=P8) == ALIGN
+    assert go(a0=P + 1) == ALIGN and go(a4=P2) == ALIGN and go(a6=P2) == ALIGN and go(a10=P + 1) == ALIGN
+    assert go(a1=1, a0=P2) == ALIGN and go(a1=1, a10=P2) == ALIGN
     assert f(None, 0, 0, 64, None, 4, None, 0, 0, 1.0, None, None) == OK
 
 

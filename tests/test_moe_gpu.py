@@ -253,6 +253,27 @@ def test_route_backward_repeated_and_foreign_indices():
         assert np.all(np.abs(f64(out) - want) <= 2.0 ** -16 * mag + 2.0 ** -24 * np.abs(want) + 2.0 ** -120)
 
 
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_route_of_rows_off_the_wide_boundaries(dt):
+    """Logits and gradients that start anywhere: slices of larger tensors."""
+    for E, skip in ((64, 1), (256, 3), (128, 5), (16, 7)):
+        big = torch.randn(9 * E + 16, generator=gen(E)).to(dt).cuda()
+        x = big[skip:skip + 9 * E].view(9, E)
+        w, ids = empty(F32, 9, 4), empty(torch.int32, 9, 4)
+        mxq.moe_route(x, w, ids)
+        w2, ids2 = empty(F32, 9, 4), empty(torch.int32, 9, 4)
+        mxq.moe_route(x.clone(), w2, ids2)
+        assert torch.equal(w, w2) and torch.equal(ids, ids2)
+        gw = torch.randn(9, 4, generator=gen(1)).cuda()
+        buf = empty(dt, 9 * E + 16)
+        mxq.moe_route_backward(x, ids, gw, buf[skip:skip + 9 * E].view(9, E))
+        want = empty(dt, 9, E)
+        mxq.moe_route_backward(x.clone(), ids, gw, want)
+        assert torch.equal(buf[skip:skip + 9 * E].view(9, E), want)
+        rest = torch.cat((buf[:skip], buf[skip + 9 * E:])).view(torch.uint8)
+        assert (rest == 0xA5).all()
+
+
 def test_route_many_rows_are_all_written():
     """More rows than one pass of the grid covers; every row against the plain rule."""
     T, E, k = 30011, 16, 1
@@ -656,9 +677,10 @@ def test_the_operators_together(T):
     assert np.all(np.abs(f64(out) - want) <= tol)
 
 
-def test_the_operators_in_a_graph_on_their_own_stream():
+@pytest.mark.parametrize("T", [40, 5000])
+def test_the_operators_in_a_graph_on_their_own_stream(T):
     """The whole chain captured into a CUDA graph and replayed on new inputs."""
-    T, D, E, N, k = 40, 512, 8, 256, 2
+    T, D, E, N, k = T, 512, 8, 256, 2
     x, res, w = norm_inputs(T, D, BF, 1)
     g = gen(2)
     router = (torch.randn(E, D, generator=g) / D ** 0.5).cuda()
