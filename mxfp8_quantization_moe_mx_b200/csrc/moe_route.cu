@@ -373,8 +373,8 @@ struct __align__(16) Picked {
 __device__ __forceinline__ int before(float o, float v, bool earlier) { return o > v || (o == v && earlier); }
 
 template <int NI, typename L>
-__device__ __forceinline__ bool select_few(const float (&c)[NI], const RouteArgs& a, const L* row, float slack,
-                                           float top, int lane, Picked* s, int& id) {
+__device__ __forceinline__ bool select_few(const float (&c)[NI], const RouteArgs& a, bool have_bias, int score,
+                                           const L* row, float slack, float top, int lane, Picked* s, int& id) {
     const float NEG = neg_inf<float>();
     float h = c[0];
 #pragma unroll
@@ -413,10 +413,10 @@ __device__ __forceinline__ bool select_few(const float (&c)[NI], const RouteArgs
         v = s->val[lane];
         e = s->id[lane];
     }
-    if (a.bias) {
+    if (have_bias) {
         if (lane < cnt) {
             b = __ldg(a.bias + e);
-            err = cand_err(a.score, fabsf(v - b), v);
+            err = cand_err(score, fabsf(v - b), v);
         }
         s->val[lane] = v;  // the places behind the last hold -inf
         s->err[lane] = err;
@@ -431,8 +431,8 @@ __device__ __forceinline__ bool select_few(const float (&c)[NI], const RouteArgs
                     (fabsf(o.w - v) <= err + f.w);
         }
         if (__any_sync(FULL_MASK, near > 1)) {
-            const double sum = a.score == 0 ? exact_sum<NI, L>(row, a.E, (double)top, lane) : 1.0;
-            const double x = lane < cnt ? exact_candidate(ld_logit(row + e), b, a.score, (double)top, sum) : 0.0;
+            const double sum = score == 0 ? exact_sum<NI, L>(row, a.E, (double)top, lane) : 1.0;
+            const double x = lane < cnt ? exact_candidate(ld_logit(row + e), b, score, (double)top, sum) : 0.0;
             rank = 0;
             for (int j = 0; j < cnt; ++j) {
                 const double o = __shfl_sync(FULL_MASK, x, j);
@@ -470,7 +470,10 @@ __device__ __noinline__ int choose_exact(const L* row, RouteArgs a, double* sc, 
     return id;
 }
 
-template <int NI, typename L>
+// MODE: what is known when the kernel is compiled, which frees registers and a quarter of the
+// instructions (65536 x 256 in 8 groups: 59 us against 77).
+enum { ROUTE_ANY = 0, ROUTE_SIGMOID_BIAS_GROUPS = 1, ROUTE_SIGMOID_BIAS = 2, ROUTE_PLAIN = 3 };
+template <int NI, typename L, int MODE>
 __global__ void __launch_bounds__(32 * RT_WARPS, NI <= 8 ? 4 : NI <= 16 ? 2 : 1) moe_route_kernel(const L* __restrict__ logits, RouteArgs a,
                                                                   float* __restrict__ weights,
                                                                   int32_t* __restrict__ ids) {
@@ -481,11 +484,13 @@ __global__ void __launch_bounds__(32 * RT_WARPS, NI <= 8 ? 4 : NI <= 16 ? 2 : 1)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t n_warps = (int64_t)gridDim.x * RT_WARPS;
     const bool vec = a.aligned && row_vec<NI, L>(a.E);
-    const bool have_bias = a.bias != nullptr, grouped = a.n_groups > 1;
+    const bool have_bias = MODE == ROUTE_ANY ? a.bias != nullptr : MODE != ROUTE_PLAIN;
+    const bool grouped = MODE == ROUTE_ANY ? a.n_groups > 1 : MODE == ROUTE_SIGMOID_BIAS_GROUPS;
+    const int score = MODE == ROUTE_SIGMOID_BIAS_GROUPS || MODE == ROUTE_SIGMOID_BIAS ? 1 : a.score;
     const bool by_p = grouped && !have_bias && a.group_top == 2;  // groups by scores, candidates logits
     const bool need_p = have_bias || by_p;
     const int gs = a.gs, gl_log = a.gl_log, gl = 1 << (gl_log < 0 ? 0 : gl_log);
-    const bool runs = gl_log >= 0;
+    const bool runs = MODE == ROUTE_SIGMOID_BIAS_GROUPS || gl_log >= 0;
     float* row_s = reinterpret_cast<float*>(route_rows + (int64_t)warp * a.E);
     constexpr bool KEEP_BIAS = NI <= 8;  // the lane's biases stay in registers
     float bias[KEEP_BIAS ? NI : 1];
@@ -512,10 +517,10 @@ __global__ void __launch_bounds__(32 * RT_WARPS, NI <= 8 ? 4 : NI <= 16 ? 2 : 1)
             c[i] = l[i];
         }
         top = redux_max_nan(top);
-        const bool softmax_sum = a.score == 0 && (need_p || !a.renorm);
+        const bool softmax_sum = score == 0 && (need_p || !a.renorm);
         if (need_p || softmax_sum) {
             float p[NI];
-            if (a.score == 1) {
+            if (score == 1) {
 #pragma unroll
                 for (int i = 0; i < NI; ++i) {
                     const float u = __expf(-fabsf(l[i])), inv = rcp1(1.0f + u);
@@ -550,7 +555,7 @@ __global__ void __launch_bounds__(32 * RT_WARPS, NI <= 8 ? 4 : NI <= 16 ? 2 : 1)
                     if (l[i] != NEG) c[i] = p[i];  // for the groups; the logits come back below
             }
         }
-        if (isnan(top) || (a.score == 0 && top == INF)) {
+        if (isnan(top) || (score == 0 && top == INF)) {
             if (lane < a.k) {
                 weights[t * a.k + lane] = __int_as_float(0x7FC00000);
                 ids[t * a.k + lane] = lane;
@@ -612,7 +617,7 @@ __global__ void __launch_bounds__(32 * RT_WARPS, NI <= 8 ? 4 : NI <= 16 ? 2 : 1)
                 const float hi = redux_max(h);
                 if (hi > NEG) {
                     const float err = by_p ? (lo + hi) * (2.0f * RT_REL) + 0x1p-120f
-                                           : 4.0f * score_err(a.score) + (bias_mag + 1.0f) * 0x1p-19f;
+                                           : 4.0f * score_err(score) + (bias_mag + 1.0f) * 0x1p-19f;
                     sure = lo - hi > err;  // false where both are infinite
                 }
             }
@@ -632,8 +637,8 @@ __global__ void __launch_bounds__(32 * RT_WARPS, NI <= 8 ? 4 : NI <= 16 ? 2 : 1)
         int id = -1;
         if (sure) {
             // no finite candidate is further than half of this from its exact value
-            const float slack = have_bias ? 2.0f * score_err(a.score) + (bias_mag + 1.0f) * 0x1p-20f : 0.0f;
-            if (a.k > 16 || !select_few<NI, L>(c, a, row, slack, top, lane, &picked[warp], id)) {
+            const float slack = have_bias ? 2.0f * score_err(score) + (bias_mag + 1.0f) * 0x1p-20f : 0.0f;
+            if (a.k > 16 || !select_few<NI, L>(c, a, have_bias, score, row, slack, top, lane, &picked[warp], id)) {
                 // with a bias one more than k, to see that the order is beyond doubt
                 int last_id = -1;
                 float val = NEG, last_val = NEG;
@@ -642,7 +647,7 @@ __global__ void __launch_bounds__(32 * RT_WARPS, NI <= 8 ? 4 : NI <= 16 ? 2 : 1)
                 if (have_bias) {
                     // each against the next one: lane j has the j-th, every lane the last
                     const float lj = id >= 0 ? ld_logit(row + id) : 0.0f, bj = id >= 0 ? __ldg(a.bias + id) : 0.0f;
-                    const float err = cand_err(a.score, fabsf(val - bj), val);
+                    const float err = cand_err(score, fabsf(val - bj), val);
                     int nid = __shfl_down_sync(FULL_MASK, id, 1);
                     float nv = __shfl_down_sync(FULL_MASK, val, 1), nl = __shfl_down_sync(FULL_MASK, lj, 1),
                           nb = __shfl_down_sync(FULL_MASK, bj, 1), ne = __shfl_down_sync(FULL_MASK, err, 1);
@@ -651,7 +656,7 @@ __global__ void __launch_bounds__(32 * RT_WARPS, NI <= 8 ? 4 : NI <= 16 ? 2 : 1)
                         nv = last_val;
                         nl = nid >= 0 ? ld_logit(row + nid) : 0.0f;
                         nb = nid >= 0 ? __ldg(a.bias + nid) : 0.0f;
-                        ne = cand_err(a.score, fabsf(nv - nb), nv);
+                        ne = cand_err(score, fabsf(nv - nb), nv);
                     }
                     const bool close = id >= 0 && nid >= 0 && !(val - nv > err + ne) && !(lj == nl && bj == nb) &&
                                        fabsf(val) < INF;  // infinite candidates tie by index, exactly
@@ -664,7 +669,7 @@ __global__ void __launch_bounds__(32 * RT_WARPS, NI <= 8 ? 4 : NI <= 16 ? 2 : 1)
         const bool mine = lane < a.k && id >= 0;
         const float lj = mine ? ld_logit(row + id) : NEG;
         float w = 0.0f;
-        if (a.score == 1) {
+        if (score == 1) {
             const float u = expf(-fabsf(lj)), inv = rcp1(1.0f + u);
             w = !mine ? 0.0f : lj < 0.0f ? u * inv : inv;
             if (a.renorm) w = __fdividef(w, warp_sum(w) + 1e-20f);
@@ -866,8 +871,18 @@ cudaError_t launch_moe_route(const void* logits, bool bf16, int64_t T, int E, co
             }
             return launch_dependent(kernel, route_grid(T), 32 * RT_WARPS, smem, stream, l, a, weights, ids);
         };
-        return bf16 ? go(moe_route_kernel<NI, uint16_t>, static_cast<const uint16_t*>(logits))
-                    : go(moe_route_kernel<NI, float>, static_cast<const float*>(logits));
+        auto typed = [&](auto mode) {
+            constexpr int MODE = decltype(mode)::value;
+            return bf16 ? go(moe_route_kernel<NI, uint16_t, MODE>, static_cast<const uint16_t*>(logits))
+                        : go(moe_route_kernel<NI, float, MODE>, static_cast<const float*>(logits));
+        };
+        if constexpr (NI <= 8) {  // rows of more than 256: the general form alone
+            if (bias && score == 1 && n_groups > 1 && a.gl_log >= 0)
+                return typed(std::integral_constant<int, ROUTE_SIGMOID_BIAS_GROUPS>());
+            if (bias && score == 1 && n_groups == 1) return typed(std::integral_constant<int, ROUTE_SIGMOID_BIAS>());
+            if (!bias && n_groups == 1) return typed(std::integral_constant<int, ROUTE_PLAIN>());
+        }
+        return typed(std::integral_constant<int, ROUTE_ANY>());
     });
 }
 
