@@ -20,7 +20,7 @@
 
 #include <algorithm>
 
-#include "mxq_device.cuh"
+#include "dependent.cuh"
 #include "mxq_launch.h"
 
 namespace mxq {

@@ -21,7 +21,7 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "mxq_device.cuh"
+#include "dependent.cuh"
 #include "mxq_launch.h"
 
 namespace mxq {

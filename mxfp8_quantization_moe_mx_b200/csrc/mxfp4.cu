@@ -10,7 +10,7 @@
 
 #include <algorithm>
 
-#include "mxq_device.cuh"
+#include "dependent.cuh"
 #include "mxq_launch.h"
 
 namespace mxq {

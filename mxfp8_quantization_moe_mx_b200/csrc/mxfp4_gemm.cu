@@ -25,6 +25,7 @@
 #include <algorithm>
 #include <cstring>
 
+#include "dependent.cuh"
 #include "mxq_launch.h"
 #include "tc_pair.cuh"
 

@@ -19,7 +19,7 @@
 #include <type_traits>
 
 #include "mxq.h"
-#include "mxq_device.cuh"
+#include "dependent.cuh"
 #include "mxq_launch.h"
 
 namespace mxq {
@@ -174,45 +174,63 @@ __device__ __forceinline__ void ring_leave(Ring* ring, int stages, int st, uint3
     atomicAdd(&g_norm_timeouts, 1u);
 }
 
-// One row's norm and codes from its packed sums h[] (V vectors per thread), stored.
+// A block's codes (eight per lane) and its scale, where a block may hold Inf or NaN (SPECIAL)
+// or not.
+template <bool SPECIAL>
+__device__ __forceinline__ uint2 codes8(const uint4& o, uint32_t b) {
+    if (SPECIAL && b == 255u) return make_uint2(nan4(o.x, o.y), nan4(o.z, o.w));
+    const float mul = mx_mult(b);
+    return make_uint2(quant4(o.x, o.y, mul), quant4(o.z, o.w, mul));
+}
+
+// One row's norm and codes from its packed sums h[] (V vectors per thread), stored.  `base`:
+// the element of the thread's first vector; the others follow 256 elements apart.
 template <int V, typename W>
-__device__ __forceinline__ void norm_row(const uint4 (&h)[V], const W8<W> (&w)[V], float r, int64_t at, int nv,
+__device__ __forceinline__ void norm_row(const uint4 (&h)[V], const W8<W> (&w)[V], float r, int64_t base, int nv,
                                          uint16_t* y, uint8_t* __restrict__ q, uint8_t* __restrict__ s) {
     const int lane = threadIdx.x & 31;
-    uint32_t mine = 0;  // lane l < 8 V: the scale of the warp's block l
+    uint4 o[V];
+    uint32_t am[V], top = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int v = vec_of<V>(i);
         uint32_t p[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const f2 f = mul2(mul2(bf2(word(h[i], j)), f2{r, r}), w[i].pair(j));
             p[j] = cvt_bf16x2(f.x, f.y);
         }
-        const uint4 o = make_uint4(p[0], p[1], p[2], p[3]);
-        uint32_t am = mag2(amax2(amax2(o.x, o.y), amax2(o.z, o.w)));
-        am = max(am & 0xFFFFu, am >> 16);
-        am = max(am, __shfl_xor_sync(FULL_MASK, am, 1));
-        am = max(am, __shfl_xor_sync(FULL_MASK, am, 2));
-        const uint32_t b = e8m0_of_amax(am);
-        uint2 c;
-        if (b != 255u) {
-            const float mul = mx_mult(b);
-            c.x = quant4(o.x, o.y, mul);
-            c.y = quant4(o.z, o.w, mul);
-        } else {
-            c.x = nan4(o.x, o.y);
-            c.y = nan4(o.z, o.w);
+        o[i] = make_uint4(p[0], p[1], p[2], p[3]);
+        uint32_t m = mag2(amax2(amax2(p[0], p[1]), amax2(p[2], p[3])));
+        m = max(m & 0xFFFFu, m >> 16);
+        m = max(m, __shfl_xor_sync(FULL_MASK, m, 1));
+        am[i] = max(m, __shfl_xor_sync(FULL_MASK, m, 2));
+        top = max(top, am[i]);
+    }
+    if (y) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (vec_of<V>(i) < nv) *reinterpret_cast<uint4*>(y + base + 256 * i) = o[i];
+    }
+    uint32_t mine = 0;  // lane l < 8 V: the scale of the warp's block l
+    if (!__any_sync(FULL_MASK, top >= 0x7F80u)) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const uint32_t b = e8m0_of_finite_amax(am[i]);
+            if (vec_of<V>(i) < nv) *reinterpret_cast<uint2*>(q + base + 256 * i) = codes8<false>(o[i], b);
+            const uint32_t t = __shfl_sync(FULL_MASK, b, (lane & 7) * 4);
+            if ((lane >> 3) == i) mine = t;
         }
-        if (v < nv) {
-            if (y) *reinterpret_cast<uint4*>(y + at + 8 * v) = o;
-            *reinterpret_cast<uint2*>(q + at + 8 * v) = c;
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const uint32_t b = e8m0_of_amax(am[i]);
+            if (vec_of<V>(i) < nv) *reinterpret_cast<uint2*>(q + base + 256 * i) = codes8<true>(o[i], b);
+            const uint32_t t = __shfl_sync(FULL_MASK, b, (lane & 7) * 4);
+            if ((lane >> 3) == i) mine = t;
         }
-        const uint32_t t = __shfl_sync(FULL_MASK, b, (lane & 7) * 4);
-        if ((lane >> 3) == i) mine = t;
     }
     const int block = (int)(threadIdx.x >> 5) * 8 * V + lane;
-    if (lane < 8 * V && block < nv / 4) s[(at >> 5) + block] = (uint8_t)mine;
+    if (lane < 8 * V && block < nv / 4) s[(base - 8 * vec_of<V>(0)) / 32 + block] = (uint8_t)mine;
 }
 
 template <int V>
@@ -238,7 +256,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_mx_few_kernel(const uint16_t* x,
     __shared__ float part[64];
     grid_wait();
     const int nv = D / 8;
-    const int64_t m = blockIdx.x, at = m * D;
+    const int64_t m = blockIdx.x, base = m * D + 8 * vec_of<V>(0);
     uint4 h[V];
     W8<W> g[V] = {};
 #pragma unroll
@@ -247,25 +265,28 @@ __global__ void __launch_bounds__(1024) rmsnorm_mx_few_kernel(const uint16_t* x,
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int v = vec_of<V>(i);
-        h[i] = v < nv ? ld_v4(x + at + 8 * v) : make_uint4(0, 0, 0, 0);
-        if (residual && v < nv) h[i] = add8(h[i], ld_v4(residual + at + 8 * v));
+        h[i] = v < nv ? ld_v4(x + base + 256 * i) : make_uint4(0, 0, 0, 0);
+        if (residual && v < nv) h[i] = add8(h[i], ld_v4(residual + base + 256 * i));
     }
     if (res_out) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int v = vec_of<V>(i);
-            if (v < nv) *reinterpret_cast<uint4*>(res_out + at + 8 * v) = h[i];
+            if (v < nv) *reinterpret_cast<uint4*>(res_out + base + 256 * i) = h[i];
         }
     }
     const float r = __frsqrt_rn(cta_sum(sum_squares<V>(h), part, 0) / (float)D + eps);
     if (rstd && threadIdx.x == 0) rstd[m] = r;
-    norm_row<V, W>(h, g, r, at, nv, y, q, s);
+    norm_row<V, W>(h, g, r, base, nv, y, q, s);
 }
 
 // Many rows.  V 8-element vectors per thread; D / 8 <= V * blockDim.x; RES: with a residual.
 // Held to 64 registers for five CTAs of 160 threads (D = 5120) on an SM.  65536 x 5120 with a
-// residual: 395 us, 5.97 TB/s, 91% of a copy (four CTAs at 88 registers 406 us; two vectors
-// per thread 410; the weights read again for every row, after its reduction, 416).
+// residual: 395 us, 5.97 TB/s, 91% of a copy (four CTAs 406-418 us; two vectors per thread
+// 410; the weights read again for every row, after its reduction, 416).  In a long loop the
+// card's power limit sets the pace: 400-410 us, and 440 before the blocks' NaN checks were
+// taken out of the common path and the addresses out of the vectors' loop (248 to 217
+// million warp instructions).
 template <int V, typename W, bool RES>
 __global__ void __launch_bounds__(512, 2) rmsnorm_mx_kernel(const uint16_t* x, const uint16_t* residual,
                                                          const W* __restrict__ w, int64_t M, int D, float eps,
@@ -286,16 +307,17 @@ __global__ void __launch_bounds__(512, 2) rmsnorm_mx_kernel(const uint16_t* x, c
         if (vec_of<V>(i) < nv) g[i].load(w + 8 * vec_of<V>(i));
     int st = 0, turn = 0;
     uint32_t phase = 0;
+    const uint32_t row0 = smem_addr(norm_sm) + 16 * vec_of<V>(0);  // vectors of a thread: 512 bytes apart
     for (int64_t m = blockIdx.x; m < M; m += gridDim.x, turn ^= 1) {
-        const int64_t at = m * D;
+        const int64_t base = m * D + 8 * vec_of<V>(0);
         if (!mbar_wait_bounded(&ring.full[st], phase, NORM_WAIT_NS)) ring.abort = 1;
-        const uint8_t* row = norm_sm + (size_t)st * N * D * 2;
+        const uint32_t row = row0 + (uint32_t)(st * N * D * 2);
         uint4 h[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int v = vec_of<V>(i);
-            h[i] = v < nv ? lds_v4(row + 16 * v) : make_uint4(0, 0, 0, 0);
-            if (RES && v < nv) h[i] = add8(h[i], lds_v4(row + 2 * D + 16 * v));
+            const bool in = vec_of<V>(i) < nv;
+            h[i] = in ? lds_v4_at(row + 512 * i) : make_uint4(0, 0, 0, 0);
+            if (RES && in) h[i] = add8(h[i], lds_v4_at(row + 2 * D + 512 * i));
         }
         const float sum = cta_sum(sum_squares<V>(h), part, turn, true);  // with a barrier: the stage is read
         if (*(volatile int*)&ring.abort) {
@@ -314,12 +336,12 @@ __global__ void __launch_bounds__(512, 2) rmsnorm_mx_kernel(const uint16_t* x, c
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const int v = vec_of<V>(i);
-                if (v < nv) *reinterpret_cast<uint4*>(res_out + at + 8 * v) = h[i];
+                if (v < nv) *reinterpret_cast<uint4*>(res_out + base + 256 * i) = h[i];
             }
         }
         const float r = __frsqrt_rn(sum / (float)D + eps);
         if (rstd && tid == 0) rstd[m] = r;
-        norm_row<V, W>(h, g, r, at, nv, y, q, s);
+        norm_row<V, W>(h, g, r, base, nv, y, q, s);
     }
 }
 
@@ -350,11 +372,12 @@ __global__ void __launch_bounds__(512) rmsnorm_backward_kernel(
     f2 gw[V][4] = {};
     int st = 0, turn = 0;
     uint32_t phase = 0;
+    const uint32_t row0 = smem_addr(norm_sm) + 16 * vec_of<V>(0);
     for (int64_t m = blockIdx.x; m < M; m += gridDim.x, turn ^= 1) {
-        const int64_t at = m * D;
+        const int64_t base = m * D + 8 * vec_of<V>(0);
         const float r = __ldg(rstd + m);
         if (!mbar_wait_bounded(&ring.full[st], phase, NORM_WAIT_NS)) ring.abort = 1;
-        const uint8_t* row = norm_sm + (size_t)st * N * D * 2;
+        const uint32_t row = row0 + (uint32_t)(st * N * D * 2);
         uint4 a[V], b[V], e[V];
         f2 dot = {0.0f, 0.0f};
 #pragma unroll
@@ -362,9 +385,9 @@ __global__ void __launch_bounds__(512) rmsnorm_backward_kernel(
             const int v = vec_of<V>(i);
             a[i] = b[i] = e[i] = make_uint4(0, 0, 0, 0);
             if (v >= nv) continue;
-            a[i] = lds_v4(row + 16 * v);
-            b[i] = lds_v4(row + 2 * D + 16 * v);
-            if (RES) e[i] = lds_v4(row + 4 * D + 16 * v);
+            a[i] = lds_v4_at(row + 512 * i);
+            b[i] = lds_v4_at(row + 2 * D + 512 * i);
+            if (RES) e[i] = lds_v4_at(row + 4 * D + 512 * i);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const f2 f = bf2(word(a[i], j)), n = mul2(bf2(word(b[i], j)), f2{r, r});
@@ -398,7 +421,7 @@ __global__ void __launch_bounds__(512) rmsnorm_backward_kernel(
                 if (RES) t = fma2(bf2(word(e[i], j)), f2{1.0f, 1.0f}, t);
                 o[j] = cvt_bf16x2(t.x, t.y);
             }
-            *reinterpret_cast<uint4*>(gx + at + 8 * v) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4*>(gx + base + 256 * i) = make_uint4(o[0], o[1], o[2], o[3]);
         }
     }
     float* mine = partial + (int64_t)blockIdx.x * D;
