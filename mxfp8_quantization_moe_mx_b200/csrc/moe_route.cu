@@ -7,16 +7,16 @@
 // candidates, ties to the lower index.  Weights from p, see include/mxq.h.
 //
 // The choice is that of the formula in 64 bits.  The kernel computes p and c in 32 bits
-// with a known error and compares: where two candidates (or two groups at the border)
-// that the order depends on lie closer than that error allows, and are not the same
-// logit and the same bias, the row's scores are computed again in 64 bits and the choice
-// repeated.  With scores spread as a router's are, that happens in well under one row of
-// a hundred, so the 64-bit pass costs nothing on average.
+// with a known error and compares: where two candidates that the order depends on lie closer
+// than that error allows, the few candidates in question are computed again in 64 bits; where
+// two groups at the border do, the whole row is.  With scores spread as a router's are, that
+// happens in 0.2% of the rows, so the 64-bit part costs nothing on average.
 //
 // One warp per row.  Lane l holds the NI consecutive elements l NI .. l NI + NI - 1 (NI the
 // power of two that covers E), so that the lowest index of equal candidates is the lowest
 // lane's, a group is a run of lanes, and a row loads in 16-byte pieces.  Bound by
-// instruction issue: a row of 256 in 8 groups takes about 600 warp instructions.
+// instruction issue: a row of 256 in 8 groups with a bias takes about 750 warp instructions
+// (65536 rows: 59 us, 1.2 TB/s), a row of 128 without either about 500.
 
 #include <algorithm>
 #include <type_traits>
@@ -72,11 +72,10 @@ __device__ __forceinline__ R warp_sum(R v) {
 }
 
 // The warp's largest (value, lowest index on ties); returned to every lane.
-template <typename R>
-__device__ __forceinline__ void warp_argmax(R& v, int& idx) {
+__device__ __forceinline__ void warp_argmax(double& v, int& idx) {
 #pragma unroll
     for (int s = 16; s; s >>= 1) {
-        const R ov = __shfl_xor_sync(FULL_MASK, v, s);
+        const double ov = __shfl_xor_sync(FULL_MASK, v, s);
         const int oi = __shfl_xor_sync(FULL_MASK, idx, s);
         if (ov > v || (ov == v && oi < idx)) {
             v = ov;
@@ -94,16 +93,16 @@ struct RouteArgs {
     bool aligned;    // the row arrays start on 16-byte boundaries
 };
 
-// Scores of the lane's elements (softmax over the whole row, or sigmoid); masked (-inf)
-// and absent elements get 0.
-template <int NI, typename R>
-__device__ __forceinline__ void scores(const float (&l)[NI], int score, R (&p)[NI]) {
+// Scores of the lane's elements in 64 bits (softmax over the whole row, or sigmoid); masked
+// (-inf) and absent elements get 0.
+template <int NI>
+__device__ __forceinline__ void scores_in_64(const float (&l)[NI], int score, double (&p)[NI]) {
     if (score == 1) {
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-            R q;
-            sigmoid_pair<R>((R)l[i], p[i], q);
-            if (l[i] == neg_inf<float>()) p[i] = (R)0;
+            double q;
+            sigmoid_pair<double>((double)l[i], p[i], q);
+            if (l[i] == neg_inf<float>()) p[i] = 0.0;
         }
         return;
     }
@@ -111,14 +110,14 @@ __device__ __forceinline__ void scores(const float (&l)[NI], int score, R (&p)[N
 #pragma unroll
     for (int i = 0; i < NI; ++i) m = fmaxf(m, l[i]);
     m = warp_max(m);
-    R sum = (R)0;
+    double sum = 0.0;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-        p[i] = l[i] == neg_inf<float>() ? (R)0 : exp_((R)l[i] - (R)m);
+        p[i] = l[i] == neg_inf<float>() ? 0.0 : exp((double)l[i] - (double)m);
         sum += p[i];
     }
     sum = warp_sum(sum);
-    const R inv = sum > (R)0 ? (R)1 / sum : (R)0;
+    const double inv = sum > 0.0 ? 1.0 / sum : 0.0;
 #pragma unroll
     for (int i = 0; i < NI; ++i) p[i] *= inv;
 }
@@ -147,7 +146,7 @@ __device__ __forceinline__ void choose_in_64(const float (&l)[NI], const RouteAr
     const bool have_bias = a.bias != nullptr;
     const bool by_p = a.n_groups > 1 && !have_bias && a.group_top == 2;
     double c[NI], p[NI];
-    scores<NI, double>(l, a.score, p);
+    scores_in_64<NI>(l, a.score, p);
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
         const int e = lane + 32 * i;
@@ -349,7 +348,7 @@ __device__ __forceinline__ double exact_candidate(float l, float b, int score, d
 }
 
 // Softmax's sum over the row in 64 bits, to every lane.
-template <int NI, typename L>
+template <typename L>
 __device__ __noinline__ double exact_sum(const L* row, int E, double max, int lane) {
     double s = 0.0;
 #pragma unroll 1
@@ -431,7 +430,7 @@ __device__ __forceinline__ bool select_few(const float (&c)[NI], const RouteArgs
                     (fabsf(o.w - v) <= err + f.w);
         }
         if (__any_sync(FULL_MASK, near > 1)) {
-            const double sum = score == 0 ? exact_sum<NI, L>(row, a.E, (double)top, lane) : 1.0;
+            const double sum = score == 0 ? exact_sum<L>(row, a.E, (double)top, lane) : 1.0;
             const double x = lane < cnt ? exact_candidate(ld_logit(row + e), b, score, (double)top, sum) : 0.0;
             rank = 0;
             for (int j = 0; j < cnt; ++j) {
@@ -474,9 +473,9 @@ __device__ __noinline__ int choose_exact(const L* row, RouteArgs a, double* sc, 
 // instructions (65536 x 256 in 8 groups: 59 us against 77).
 enum { ROUTE_ANY = 0, ROUTE_SIGMOID_BIAS_GROUPS = 1, ROUTE_SIGMOID_BIAS = 2, ROUTE_PLAIN = 3 };
 template <int NI, typename L, int MODE>
-__global__ void __launch_bounds__(32 * RT_WARPS, NI <= 8 ? 4 : NI <= 16 ? 2 : 1) moe_route_kernel(const L* __restrict__ logits, RouteArgs a,
-                                                                  float* __restrict__ weights,
-                                                                  int32_t* __restrict__ ids) {
+__global__ void __launch_bounds__(32 * RT_WARPS, NI <= 8 ? 4 : NI <= 16 ? 2 : 1)
+    moe_route_kernel(const L* __restrict__ logits, RouteArgs a, float* __restrict__ weights,
+                     int32_t* __restrict__ ids) {
     extern __shared__ double route_rows[];
     __shared__ Picked picked[RT_WARPS];
     grid_wait();
@@ -645,20 +644,18 @@ __global__ void __launch_bounds__(32 * RT_WARPS, NI <= 8 ? 4 : NI <= 16 ? 2 : 1)
                 extract<NI>(c, have_bias ? a.k + 1 : a.k, lane, id, val, last_id, last_val);
                 if (lane >= a.k) id = -1;
                 if (have_bias) {
-                    // each against the next one: lane j has the j-th, every lane the last
-                    const float lj = id >= 0 ? ld_logit(row + id) : 0.0f, bj = id >= 0 ? __ldg(a.bias + id) : 0.0f;
-                    const float err = cand_err(score, fabsf(val - bj), val);
+                    // each against the next one (lane j has the j-th, every lane the last), all
+                    // with the error of the row's largest score: any candidate further down is
+                    // then further away than its own error, too
+                    const float pmax = score == 1 ? 1.0f : 1.0f / sum;
                     int nid = __shfl_down_sync(FULL_MASK, id, 1);
-                    float nv = __shfl_down_sync(FULL_MASK, val, 1), nl = __shfl_down_sync(FULL_MASK, lj, 1),
-                          nb = __shfl_down_sync(FULL_MASK, bj, 1), ne = __shfl_down_sync(FULL_MASK, err, 1);
+                    float nv = __shfl_down_sync(FULL_MASK, val, 1);
                     if (lane == a.k - 1) {
                         nid = last_id;
                         nv = last_val;
-                        nl = nid >= 0 ? ld_logit(row + nid) : 0.0f;
-                        nb = nid >= 0 ? __ldg(a.bias + nid) : 0.0f;
-                        ne = cand_err(score, fabsf(nv - nb), nv);
                     }
-                    const bool close = id >= 0 && nid >= 0 && !(val - nv > err + ne) && !(lj == nl && bj == nb) &&
+                    const float err = 2.0f * cand_err(score, pmax, bias_mag + 1.0f);
+                    const bool close = id >= 0 && nid >= 0 && !(val - nv > err) &&
                                        fabsf(val) < INF;  // infinite candidates tie by index, exactly
                     sure = !__any_sync(FULL_MASK, close);
                 }

@@ -156,6 +156,23 @@ def test_route_order_of_close_candidates():
         check_route(x, 8, b, score=score, n_groups=8, top_groups=2, group_top=2)
 
 
+@pytest.mark.parametrize("k", [4, 12, 20, 32])
+def test_route_candidate_with_a_large_score_among_small_ones(k):
+    """One expert takes most of the softmax and its bias brings it down among the others: its
+    candidate's error in 32 bits is a thousand times its neighbours', and sweeps past them."""
+    g = gen(13)
+    E, T = 64, 600
+    x = 0.5 * torch.randn(1, E, generator=g).repeat(T, 1)
+    x[:, 5] = 7.0 + torch.arange(T) * 2.0 ** -19
+    b = 0.05 * torch.rand(E, generator=g)
+    p = torch.softmax(x[T // 2].double(), 0)
+    c = torch.sort(p + b, descending=True).values
+    for place in (k - 1, k, k // 2):
+        b[5] = 0.0
+        b[5] = float(c[place + 1] - p[5])
+        check_route(x, k, b)
+
+
 def test_route_large_biases_that_cancel_in_groups():
     g = gen(12)
     x = torch.randn(100, 32, generator=g)
