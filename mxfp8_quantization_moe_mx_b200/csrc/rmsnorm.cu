@@ -6,10 +6,9 @@
 //   y = bf16(h r w)
 //   q, s = 1x32 MXFP8 blocks of y     (the bytes mx_quantize gives for y)
 //
-// Everything is bound by HBM: a row is read once, by bulk copies into a ring of rows in
-// shared memory, stays in registers through the two reductions (sum of squares over the
-// CTA, block maxima over four lanes) and leaves as codes.  A CTA owns a row at a time; a
-// warp holds 32 V consecutive 8-element vectors of it, lane l the vectors l, l + 32, ..., so
+// Everything is bound by HBM: a row is read once, stays in registers through the two
+// reductions (sum of squares over the CTA, block maxima over four lanes) and leaves as codes.
+// A CTA owns a row at a time; a warp holds 32 V consecutive 8-element vectors of it, lane l the vectors l, l + 32, ..., so
 // four neighbouring lanes hold one 32-element block and a warp's 8 V scale bytes leave in one
 // run.  The sums are fp32: a thread adds
 // at most 32 squares, then 5 shuffle steps and at most 32 warps' sums, so the relative
@@ -96,10 +95,14 @@ struct W8<float> {
         return j == 0 ? f2{a.x, a.y} : j == 1 ? f2{a.z, a.w} : j == 2 ? f2{b.x, b.y} : f2{b.z, b.w};
     }
 };
-// The thread's i-th vector of its V.
+// The thread's i-th vector of its V; `warp`: which of its row's warps the thread's is.
+template <int V>
+__device__ __forceinline__ int vec_of(int i, int warp) {
+    return (warp * V + i) * 32 + (int)(threadIdx.x & 31);
+}
 template <int V>
 __device__ __forceinline__ int vec_of(int i) {
-    return ((int)(threadIdx.x >> 5) * V + i) * 32 + (int)(threadIdx.x & 31);
+    return vec_of<V>(i, (int)(threadIdx.x >> 5));
 }
 
 // Sum over the CTA, returned to every thread.  `part` holds 2 x 32 floats; `turn`
@@ -118,11 +121,140 @@ __device__ __forceinline__ float cta_sum(float v, float* part, int turn, bool ba
     return v;
 }
 
+// ---- forward -------------------------------------------------------------------------------------
+
+// A block's codes (eight per lane) and its scale, where a block may hold Inf or NaN (SPECIAL)
+// or not.
+template <bool SPECIAL>
+__device__ __forceinline__ uint2 codes8(const uint4& o, uint32_t b) {
+    if (SPECIAL && b == 255u) return make_uint2(nan4(o.x, o.y), nan4(o.z, o.w));
+    const float mul = mx_mult(b);
+    return make_uint2(quant4(o.x, o.y, mul), quant4(o.z, o.w, mul));
+}
+
+// One row's norm and codes from its packed sums h[] (V vectors per thread), stored.  `base`:
+// the element of the thread's first vector; the others follow 256 elements apart.
+template <int V, typename W>
+__device__ __forceinline__ void norm_row(const uint4 (&h)[V], const W8<W> (&w)[V], float r, int64_t base, int nv, int warp,
+                                         uint16_t* y, uint8_t* __restrict__ q, uint8_t* __restrict__ s) {
+    const int lane = threadIdx.x & 31;
+    uint4 o[V];
+    uint32_t am[V], top = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        uint32_t p[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const f2 f = mul2(mul2(bf2(word(h[i], j)), f2{r, r}), w[i].pair(j));
+            p[j] = cvt_bf16x2(f.x, f.y);
+        }
+        o[i] = make_uint4(p[0], p[1], p[2], p[3]);
+        uint32_t m = mag2(amax2(amax2(p[0], p[1]), amax2(p[2], p[3])));
+        m = max(m & 0xFFFFu, m >> 16);
+        m = max(m, __shfl_xor_sync(FULL_MASK, m, 1));
+        am[i] = max(m, __shfl_xor_sync(FULL_MASK, m, 2));
+        top = max(top, am[i]);
+    }
+    if (y) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (vec_of<V>(i, warp) < nv) *reinterpret_cast<uint4*>(y + base + 256 * i) = o[i];
+    }
+    uint32_t mine = 0;  // lane l < 8 V: the scale of the warp's block l
+    if (!__any_sync(FULL_MASK, top >= 0x7F80u)) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const uint32_t b = e8m0_of_finite_amax(am[i]);
+            if (vec_of<V>(i, warp) < nv) *reinterpret_cast<uint2*>(q + base + 256 * i) = codes8<false>(o[i], b);
+            const uint32_t t = __shfl_sync(FULL_MASK, b, (lane & 7) * 4);
+            if ((lane >> 3) == i) mine = t;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const uint32_t b = e8m0_of_amax(am[i]);
+            if (vec_of<V>(i, warp) < nv) *reinterpret_cast<uint2*>(q + base + 256 * i) = codes8<true>(o[i], b);
+            const uint32_t t = __shfl_sync(FULL_MASK, b, (lane & 7) * 4);
+            if ((lane >> 3) == i) mine = t;
+        }
+    }
+    const int block = warp * 8 * V + lane;
+    if (lane < 8 * V && block < nv / 4) s[(base - 8 * vec_of<V>(0, warp)) / 32 + block] = (uint8_t)mine;
+}
+
+template <int V>
+__device__ __forceinline__ float sum_squares(const uint4 (&h)[V]) {
+    f2 sq = {0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const f2 f = bf2(word(h[i], j));
+            sq = fma2(f, f, sq);
+        }
+    return sq.x + sq.y;
+}
+
+// V vectors per thread straight from global memory: a row's loads are all in flight at once,
+// and enough rows are on an SM to cover the reduction; nothing persists, so a CTA's exit and
+// the next one's loads overlap the others' arithmetic.  WARP_ROW: a warp per row (eight to a
+// CTA, no barrier), else a CTA per row.  65536 rows with a residual, bf16 weights:
+//   D = 5120   four vectors 342 us (6.9 TB/s; the codes of the last rows stay in L2), two 402,
+//              one 441; persistent CTAs with a ring of bulk-copied rows 395
+//   D = 16384  four 1108, two 1471;  D = 2560  173, 180;  D = 1536  106, 107
+//   D = 1024   two 72, a warp per row 79;  D = 512  a warp 39, two 69;  D = 256  21, 68
+template <int V, bool WARP_ROW, typename W>
+__global__ void __launch_bounds__(WARP_ROW ? 256 : 1024) rmsnorm_mx_kernel(
+    const uint16_t* x, const uint16_t* residual, const W* __restrict__ w, int64_t M, int D, float eps,
+    uint16_t* res_out, uint16_t* y, uint8_t* __restrict__ q, uint8_t* __restrict__ s, float* __restrict__ rstd) {
+    __shared__ float part[64];
+    grid_wait();
+    const int nv = D / 8;
+    const int warp = WARP_ROW ? 0 : (int)(threadIdx.x >> 5);
+    const int64_t first = WARP_ROW ? (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5) : blockIdx.x;
+    const int64_t step = WARP_ROW ? (int64_t)gridDim.x * 8 : gridDim.x;
+    int turn = 0;
+    for (int64_t m = first; m < M; m += step, turn ^= 1) {
+        const int64_t base = m * D + 8 * vec_of<V>(0, warp);
+        uint4 h[V];
+        W8<W> g[V] = {};
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const bool in = vec_of<V>(i, warp) < nv;
+            h[i] = in ? ld_v4(x + base + 256 * i) : make_uint4(0, 0, 0, 0);
+            if (in) g[i].load(w + 8 * vec_of<V>(i, warp));
+            if (residual && in) h[i] = add8(h[i], ld_v4(residual + base + 256 * i));
+        }
+        if (res_out) {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (vec_of<V>(i, warp) < nv) *reinterpret_cast<uint4*>(res_out + base + 256 * i) = h[i];
+        }
+        float sum = sum_squares<V>(h);
+        if (WARP_ROW) {
+#pragma unroll
+            for (int sh = 16; sh; sh >>= 1) sum += __shfl_xor_sync(FULL_MASK, sum, sh);
+        } else {
+            sum = cta_sum(sum, part, turn);
+        }
+        const float r = __frsqrt_rn(sum / (float)D + eps);
+        if (rstd && vec_of<V>(0, warp) == 0) rstd[m] = r;
+        norm_row<V, W>(h, g, r, base, nv, warp, y, q, s);
+    }
+}
+
+// ---- gradient ------------------------------------------------------------------------------------
+//
+// With n = h r and g = gy w:  gx = r (g - n mean_d(g n)) + gres,  gw = sum_m gy n.
+// A CTA walks rows blockIdx.x, + gridDim.x, ... and keeps its share of gw in registers
+// (fp32), writes it to its row of the workspace, and a second kernel adds the CTAs' rows in
+// order: no atomics, the same bits every time.
 // ---- a ring of rows in shared memory --------------------------------------------------------------
 //
-// With many rows a CTA walks rows blockIdx.x, + gridDim.x, ... and bulk copies bring its next
-// rows into shared memory while it works on one, so that the loads in flight do not depend
-// on registers or on how the reductions serialise a row.  Stage s is refilled once the
+// The gradient's CTAs persist, to keep their share of the weight's gradient.  A CTA walks rows
+// blockIdx.x, + gridDim.x, ... and bulk copies bring its next rows into shared memory while it
+// works on one, so that the loads in flight do not depend on registers or on how the
+// reductions serialise a row.  Stage s is refilled once the
 // barrier inside the row's reduction has shown that every thread has read it.  A wait that
 // runs out (see mxq_set_wait_limit_ns for how long the library's waits are by default) ends
 // the CTA: it stores nothing more, waits for its copies in flight, and is counted.
@@ -174,183 +306,6 @@ __device__ __forceinline__ void ring_leave(Ring* ring, int stages, int st, uint3
     atomicAdd(&g_norm_timeouts, 1u);
 }
 
-// A block's codes (eight per lane) and its scale, where a block may hold Inf or NaN (SPECIAL)
-// or not.
-template <bool SPECIAL>
-__device__ __forceinline__ uint2 codes8(const uint4& o, uint32_t b) {
-    if (SPECIAL && b == 255u) return make_uint2(nan4(o.x, o.y), nan4(o.z, o.w));
-    const float mul = mx_mult(b);
-    return make_uint2(quant4(o.x, o.y, mul), quant4(o.z, o.w, mul));
-}
-
-// One row's norm and codes from its packed sums h[] (V vectors per thread), stored.  `base`:
-// the element of the thread's first vector; the others follow 256 elements apart.
-template <int V, typename W>
-__device__ __forceinline__ void norm_row(const uint4 (&h)[V], const W8<W> (&w)[V], float r, int64_t base, int nv,
-                                         uint16_t* y, uint8_t* __restrict__ q, uint8_t* __restrict__ s) {
-    const int lane = threadIdx.x & 31;
-    uint4 o[V];
-    uint32_t am[V], top = 0;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        uint32_t p[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const f2 f = mul2(mul2(bf2(word(h[i], j)), f2{r, r}), w[i].pair(j));
-            p[j] = cvt_bf16x2(f.x, f.y);
-        }
-        o[i] = make_uint4(p[0], p[1], p[2], p[3]);
-        uint32_t m = mag2(amax2(amax2(p[0], p[1]), amax2(p[2], p[3])));
-        m = max(m & 0xFFFFu, m >> 16);
-        m = max(m, __shfl_xor_sync(FULL_MASK, m, 1));
-        am[i] = max(m, __shfl_xor_sync(FULL_MASK, m, 2));
-        top = max(top, am[i]);
-    }
-    if (y) {
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (vec_of<V>(i) < nv) *reinterpret_cast<uint4*>(y + base + 256 * i) = o[i];
-    }
-    uint32_t mine = 0;  // lane l < 8 V: the scale of the warp's block l
-    if (!__any_sync(FULL_MASK, top >= 0x7F80u)) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const uint32_t b = e8m0_of_finite_amax(am[i]);
-            if (vec_of<V>(i) < nv) *reinterpret_cast<uint2*>(q + base + 256 * i) = codes8<false>(o[i], b);
-            const uint32_t t = __shfl_sync(FULL_MASK, b, (lane & 7) * 4);
-            if ((lane >> 3) == i) mine = t;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const uint32_t b = e8m0_of_amax(am[i]);
-            if (vec_of<V>(i) < nv) *reinterpret_cast<uint2*>(q + base + 256 * i) = codes8<true>(o[i], b);
-            const uint32_t t = __shfl_sync(FULL_MASK, b, (lane & 7) * 4);
-            if ((lane >> 3) == i) mine = t;
-        }
-    }
-    const int block = (int)(threadIdx.x >> 5) * 8 * V + lane;
-    if (lane < 8 * V && block < nv / 4) s[(base - 8 * vec_of<V>(0)) / 32 + block] = (uint8_t)mine;
-}
-
-template <int V>
-__device__ __forceinline__ float sum_squares(const uint4 (&h)[V]) {
-    f2 sq = {0.0f, 0.0f};
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const f2 f = bf2(word(h[i], j));
-            sq = fma2(f, f, sq);
-        }
-    return sq.x + sq.y;
-}
-
-// Few rows: a CTA per row, V vectors per thread straight from global memory (two for the
-// rows of more than 8192 elements).
-template <int V, typename W>
-__global__ void __launch_bounds__(1024) rmsnorm_mx_few_kernel(const uint16_t* x, const uint16_t* residual,
-                                                              const W* __restrict__ w, int64_t M, int D, float eps,
-                                                              uint16_t* res_out, uint16_t* y, uint8_t* __restrict__ q,
-                                                              uint8_t* __restrict__ s, float* __restrict__ rstd) {
-    __shared__ float part[64];
-    grid_wait();
-    const int nv = D / 8;
-    const int64_t m = blockIdx.x, base = m * D + 8 * vec_of<V>(0);
-    uint4 h[V];
-    W8<W> g[V] = {};
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-        if (vec_of<V>(i) < nv) g[i].load(w + 8 * vec_of<V>(i));
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int v = vec_of<V>(i);
-        h[i] = v < nv ? ld_v4(x + base + 256 * i) : make_uint4(0, 0, 0, 0);
-        if (residual && v < nv) h[i] = add8(h[i], ld_v4(residual + base + 256 * i));
-    }
-    if (res_out) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int v = vec_of<V>(i);
-            if (v < nv) *reinterpret_cast<uint4*>(res_out + base + 256 * i) = h[i];
-        }
-    }
-    const float r = __frsqrt_rn(cta_sum(sum_squares<V>(h), part, 0) / (float)D + eps);
-    if (rstd && threadIdx.x == 0) rstd[m] = r;
-    norm_row<V, W>(h, g, r, base, nv, y, q, s);
-}
-
-// Many rows.  V 8-element vectors per thread; D / 8 <= V * blockDim.x; RES: with a residual.
-// Held to 64 registers for five CTAs of 160 threads (D = 5120) on an SM.  65536 x 5120 with a
-// residual: 395 us, 5.97 TB/s, 91% of a copy (four CTAs 406-418 us; two vectors per thread
-// 410; the weights read again for every row, after its reduction, 416).  In a long loop the
-// card's power limit sets the pace: 400-410 us, and 440 before the blocks' NaN checks were
-// taken out of the common path and the addresses out of the vectors' loop (248 to 217
-// million warp instructions).
-template <int V, typename W, bool RES>
-__global__ void __launch_bounds__(512, 2) rmsnorm_mx_kernel(const uint16_t* x, const uint16_t* residual,
-                                                         const W* __restrict__ w, int64_t M, int D, float eps,
-                                                         uint16_t* res_out, uint16_t* y, uint8_t* __restrict__ q,
-                                                         uint8_t* __restrict__ s, float* __restrict__ rstd,
-                                                         int stages) {
-    constexpr int N = RES ? 2 : 1;
-    extern __shared__ __align__(128) uint8_t norm_sm[];
-    __shared__ Ring ring;
-    __shared__ float part[64];
-    grid_wait();
-    const int tid = threadIdx.x, nv = D / 8;
-    const uint16_t* const from[3] = {x, residual, nullptr};
-    ring_start<N>(norm_sm, &ring, stages, from, M, D);
-    W8<W> g[V] = {};
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-        if (vec_of<V>(i) < nv) g[i].load(w + 8 * vec_of<V>(i));
-    int st = 0, turn = 0;
-    uint32_t phase = 0;
-    const uint32_t row0 = smem_addr(norm_sm) + 16 * vec_of<V>(0);  // vectors of a thread: 512 bytes apart
-    for (int64_t m = blockIdx.x; m < M; m += gridDim.x, turn ^= 1) {
-        const int64_t base = m * D + 8 * vec_of<V>(0);
-        if (!mbar_wait_bounded(&ring.full[st], phase, NORM_WAIT_NS)) ring.abort = 1;
-        const uint32_t row = row0 + (uint32_t)(st * N * D * 2);
-        uint4 h[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const bool in = vec_of<V>(i) < nv;
-            h[i] = in ? lds_v4_at(row + 512 * i) : make_uint4(0, 0, 0, 0);
-            if (RES && in) h[i] = add8(h[i], lds_v4_at(row + 2 * D + 512 * i));
-        }
-        const float sum = cta_sum(sum_squares<V>(h), part, turn, true);  // with a barrier: the stage is read
-        if (*(volatile int*)&ring.abort) {
-            ring_leave(&ring, stages, st, phase, m, M);
-            return;
-        }
-        if (tid == 0) {
-            const int64_t next = m + (int64_t)stages * gridDim.x;
-            if (next < M) ring_fill<N>(norm_sm, &ring, st, from, next * D, D);
-        }
-        if (++st == stages) {
-            st = 0;
-            phase ^= 1;
-        }
-        if (res_out) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int v = vec_of<V>(i);
-                if (v < nv) *reinterpret_cast<uint4*>(res_out + base + 256 * i) = h[i];
-            }
-        }
-        const float r = __frsqrt_rn(sum / (float)D + eps);
-        if (rstd && tid == 0) rstd[m] = r;
-        norm_row<V, W>(h, g, r, base, nv, y, q, s);
-    }
-}
-
-// ---- gradient ------------------------------------------------------------------------------------
-//
-// With n = h r and g = gy w:  gx = r (g - n mean_d(g n)) + gres,  gw = sum_m gy n.
-// A CTA walks rows blockIdx.x, + gridDim.x, ... and keeps its share of gw in registers
-// (fp32), writes it to its row of the workspace, and a second kernel adds the CTAs' rows in
-// order: no atomics, the same bits every time.
 // 16640 x 5120 with a residual's gradient: 104 us, 6.5 TB/s (the weights read again for every
 // row: 127 us; without the ring: 227).
 template <int V, typename W, bool RES>
@@ -486,24 +441,16 @@ cudaError_t launch_ring(K kernel, int v, int tensors, int64_t M, int D, int64_t 
 template <typename W>
 cudaError_t norm_forward(const uint16_t* x, const uint16_t* residual, const W* w, int64_t M, int D, float eps,
                          uint16_t* res_out, uint16_t* y, uint8_t* q, uint8_t* s, float* rstd, cudaStream_t stream) {
-    const int nv = D / 8, v = norm_vectors(nv);
-    if (M <= 2 * (int64_t)sm_count()) {
-        return nv <= 1024 ? launch_dependent(rmsnorm_mx_few_kernel<1, W>, (unsigned)M, (nv + 31) / 32 * 32, 0, stream,
-                                             x, residual, w, M, D, eps, res_out, y, q, s, rstd)
-                          : launch_dependent(rmsnorm_mx_few_kernel<2, W>, (unsigned)M, (nv + 63) / 64 * 32, 0, stream,
-                                             x, residual, w, M, D, eps, res_out, y, q, s, rstd);
-    }
-    unsigned grid = 0;
-    auto go = [&](auto vv) {
-        constexpr int V = decltype(vv)::value;
-        return residual ? launch_ring(rmsnorm_mx_kernel<V, W, true>, V, 2, M, D, INT32_MAX, &grid, stream, x, residual,
-                                      w, M, D, eps, res_out, y, q, s, rstd)
-                        : launch_ring(rmsnorm_mx_kernel<V, W, false>, V, 1, M, D, INT32_MAX, &grid, stream, x,
-                                      residual, w, M, D, eps, res_out, y, q, s, rstd);
+    const int nv = D / 8;
+    const auto go = [&](auto kernel, int64_t grid, int threads) {
+        return launch_dependent(kernel, (unsigned)std::min<int64_t>(grid, 0x7FFFFFFF), threads, 0, stream, x, residual,
+                                w, M, D, eps, res_out, y, q, s, rstd);
     };
-    return v == 1   ? go(std::integral_constant<int, 1>())
-           : v == 2 ? go(std::integral_constant<int, 2>())
-                    : go(std::integral_constant<int, 4>());
+    const int64_t eighth = M / 8 + (M % 8 != 0);
+    if (nv <= 32) return go(rmsnorm_mx_kernel<1, true, W>, eighth, 256);
+    if (nv <= 64) return go(rmsnorm_mx_kernel<2, true, W>, eighth, 256);
+    if (nv <= 128) return go(rmsnorm_mx_kernel<2, false, W>, M, (nv + 63) / 64 * 32);
+    return go(rmsnorm_mx_kernel<4, false, W>, M, (nv + 127) / 128 * 32);
 }
 
 template <typename W>
