@@ -8,7 +8,7 @@
 //
 // Bound by HBM: 2 bytes in and 17/32 out per element.  One step per warp, four 16-byte
 // vectors of bf16 per lane in it; a grid of persistent CTAs was slower in both directions, as
-// were steps of one or two vectors.  (16, 8192, 5120): quantize 260 us (6.54 TB/s; persistent
+// were steps of one or two vectors.  (16, 8192, 5120): quantize 246 us (6.91 TB/s; persistent
 // 273, two vectors 322), dequantize 252 us (6.73 TB/s; 301, 284).
 
 #include <algorithm>
@@ -101,6 +101,9 @@ __global__ void __launch_bounds__(256) f4_quant_kernel(const uint16_t* __restric
 // ---- with scales in the tensor cores' tiles: a CTA per padded 128-row tile x 512 columns
 // (16 scale columns, 4 scale tiles).  Warp w takes rows w, w + 8, ... of the tile, 1024
 // bytes of a row per step; scales gather in shared memory and leave as whole 16-byte lines.
+// 16411 x 5120 over 16 groups: 45 us, 4.7 TB/s.  What it lacks to a copy is each CTA's search
+// for its group, before its first load: CTAs of a quarter of this took 59 us, four rows a step
+// (fewer CTAs at a time) 54, one row 50.
 __global__ void __launch_bounds__(256, 5) f4_quant_blocked_kernel(const uint16_t* __restrict__ x, int64_t rows,
                                                                int64_t cols, uint8_t* __restrict__ q,
                                                                uint8_t* __restrict__ s, uint8_t* __restrict__ sf,
