@@ -739,6 +739,21 @@ __device__ __forceinline__ void store_row(uint16_t* row, int E, bool vec, int la
     }
 }
 
+// sum over the k slots m of r_m (g_j - g_m), for the lane's own slot j: what is left of
+// g_j - sum_m g_m r_m without its cancellation where one r_m is near 1 (the r_m sum to 1, up to
+// a part that the caller adds).  `pairs`: the warp's room for 32.
+__device__ __forceinline__ float pair_sum(float r, float g, int k, int lane, float2* pairs) {
+    pairs[lane] = make_float2(r, g);
+    __syncwarp();
+    float d = 0.0f;
+    for (int m = 0; m < k; ++m) {
+        const float2 o = pairs[m];
+        d = fmaf(o.x, g - o.y, d);
+    }
+    __syncwarp();
+    return d;
+}
+
 template <int NI, typename L>
 __global__ void __launch_bounds__(32 * RT_WARPS) moe_route_backward_kernel(
     const L* __restrict__ logits, RouteArgs a, const int32_t* __restrict__ ids, const float* __restrict__ gw,
@@ -746,10 +761,12 @@ __global__ void __launch_bounds__(32 * RT_WARPS) moe_route_backward_kernel(
     // a row per warp: the lanes' values lie with a stride of NI + 1, so that they meet in
     // different banks
     __shared__ float grad_rows[RT_WARPS][32 * (NI + 1)];
+    __shared__ float2 pairs_s[RT_WARPS][32];
     grid_wait();
     const float NEG = neg_inf<float>();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     float* row_s = grad_rows[warp];
+    float2* pairs = pairs_s[warp];
     const bool vec = a.aligned && row_vec<NI, L>(a.E);
     const int64_t n_warps = (int64_t)gridDim.x * RT_WARPS;
     for (int64_t t = (int64_t)blockIdx.x * RT_WARPS + warp; t < a.T; t += n_warps) {
@@ -763,11 +780,21 @@ __global__ void __launch_bounds__(32 * RT_WARPS) moe_route_backward_kernel(
         }
         const bool mine = id >= 0;
         const float lj = mine ? ld_logit(row + id) : NEG;
-        float d = 0.0f;
+        // the chosen entries are marked with their slots' numbers, which also shows whether an
+        // index comes twice
+        const int at = mine ? id / NI * (NI + 1) + id % NI : 0;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) row_s[lane * (NI + 1) + i] = 0.0f;
+        __syncwarp();
+        if (mine) row_s[at] = (float)(lane + 1);
+        __syncwarp();
+        const bool twice = __any_sync(FULL_MASK, mine && row_s[at] != (float)(lane + 1));
+        float d = 0.0f;     // the slot's part of its expert's gradient ...
+        bool whole = false;  // ... or all of it
         float base[NI];
         if (a.score == 0 && !a.renorm) {
             load_row<NI, L>(row, a.E, vec, lane, base);
-            float m = NEG, s = 0.0f;
+            float m = NEG, s = 0.0f, others = 0.0f;
 #pragma unroll
             for (int i = 0; i < NI; ++i) m = fmaxf(m, base[i]);
             m = redux_max(m);
@@ -775,12 +802,18 @@ __global__ void __launch_bounds__(32 * RT_WARPS) moe_route_backward_kernel(
             for (int i = 0; i < NI; ++i) {
                 base[i] = base[i] == NEG ? 0.0f : expf(base[i] - m);
                 s += base[i];
+                others += row_s[lane * (NI + 1) + i] == 0.0f ? base[i] : 0.0f;
             }
             s = warp_sum(s);
+            others = warp_sum(others);
             const float inv = s != 0.0f ? 1.0f / s : 0.0f;
             const float p = mine && lj != NEG ? expf(lj - m) * inv : 0.0f;
             d = g * p;
             const float f = -warp_sum(d) * inv;
+            if (!twice) {  // p (g - sum_j g_j p_j), the unchosen scores' sum taken as it is
+                d = p * fmaf(g, others * inv, pair_sum(p, g, a.k, lane, pairs));
+                whole = true;
+            }
 #pragma unroll
             for (int i = 0; i < NI; ++i) base[i] *= f;
         } else {
@@ -791,8 +824,10 @@ __global__ void __launch_bounds__(32 * RT_WARPS) moe_route_backward_kernel(
                 sigmoid_pair<float>(lj, p, q);
                 if (!mine) p = 0.0f;
                 if (a.renorm) {
-                    const float r = p / (warp_sum(p) + 1e-20f);
-                    d = r * q * (g - warp_sum(g * r));
+                    const float inv = 1.0f / (warp_sum(p) + 1e-20f), r = p * inv;
+                    // the constant's own part, down to what 64 bits hold next to 1
+                    const float rest = 1e-20f * inv > 0x1p-53f ? 1e-20f * inv : 0.0f;
+                    d = r * q * fmaf(g, rest, pair_sum(r, g, a.k, lane, pairs));
                 } else {
                     d = g * p * q;
                 }
@@ -801,14 +836,9 @@ __global__ void __launch_bounds__(32 * RT_WARPS) moe_route_backward_kernel(
                 const float ex = mine && lj > NEG ? expf(lj - m) : (lj == lj ? 0.0f : lj);
                 const float s = warp_sum(ex);
                 const float r = mine && s != 0.0f ? ex / s : 0.0f;
-                d = r * (g - warp_sum(g * r));
+                d = r * pair_sum(r, g, a.k, lane, pairs);
             }
         }
-        // whether an index comes twice: each slot leaves its number at its expert
-        const int at = mine ? id / NI * (NI + 1) + id % NI : 0;
-        if (mine) row_s[at] = (float)lane;
-        __syncwarp();
-        const bool twice = __any_sync(FULL_MASK, mine && row_s[at] != (float)lane);
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < NI; ++i) row_s[lane * (NI + 1) + i] = base[i];
@@ -820,7 +850,7 @@ __global__ void __launch_bounds__(32 * RT_WARPS) moe_route_backward_kernel(
                 __syncwarp();
             }
         } else if (mine) {
-            row_s[at] += d;
+            row_s[at] = whole ? d : row_s[at] + d;
         }
         __syncwarp();
 #pragma unroll

@@ -227,6 +227,40 @@ def test_route_backward(T, E, k, dt, score, renorm):
     assert np.all(np.abs(f64(out) - want) <= 2.0 ** -16 * mag + half * np.abs(want) + 2.0 ** -120)
 
 
+@pytest.mark.parametrize("score,renorm", [("softmax", False), ("softmax", True), ("sigmoid", True)])
+def test_route_backward_where_one_expert_has_nearly_all(score, renorm):
+    """Weights near 1 and 0: the difference g_j - sum g_m r_m is small beside its terms.  Each
+    entry, to 2^-16 of the sum of the magnitudes of its own uncancelled terms
+    r_j r_m |g_j - g_m| (and p_j p_e |g_j| for the unchosen)."""
+    g = gen(31)
+    T, E, k = 64, 24, 4
+    x = torch.randn(T, E, generator=g)
+    if score == "softmax":
+        x[:, 3] += torch.linspace(8.0, 16.0, T)
+    else:
+        x[:, 3] = 4.0
+        x[:, :3] -= 10.0
+        x[:, 4:] -= torch.linspace(8.0, 16.0, T)[:, None]
+    code = mxq.SIGMOID if score == "sigmoid" else mxq.SOFTMAX
+    ids, _ = gpu_route(x, k, score=code, renorm=renorm)
+    gw = torch.randn(T, k, generator=g)
+    out = empty(F32, T, E)
+    mxq.moe_route_backward(x.cuda(), torch.from_numpy(ids).cuda(), gw.cuda(), out, score=code, renorm=renorm)
+    want, _ = ref.route_grad(f64(x), ids, f64(gw), score, renorm, 1.0)
+    z, w = f64(x), f64(gw)
+    for t in range(T):
+        p = ref.scores(z[t], score)
+        mag = np.zeros(E)
+        r = p[ids[t]] / (p[ids[t]].sum() if renorm else 1.0)
+        f = 1.0 - p[ids[t]] if score == "sigmoid" else 1.0
+        mag[ids[t]] = f * r * (r[None, :] * np.abs(w[t][:, None] - w[t][None, :])).sum(1)
+        if not renorm:
+            rest = np.delete(np.arange(E), ids[t])
+            mag[ids[t]] += r * np.abs(w[t]) * p[rest].sum()
+            mag[rest] = p[rest] * (np.abs(w[t]) * r).sum()
+        assert np.all(np.abs(f64(out)[t] - want[t]) <= 2.0 ** -16 * mag + 2.0 ** -120)
+
+
 def test_route_backward_against_differences():
     """The gradient of a fixed choice against central differences of the 64-bit weights."""
     g = gen(21)
