@@ -292,9 +292,9 @@ int moe_route(const void* logits, int type, int64_t T, int64_t E, const float* b
  *  ids (T, k) as moe_route wrote them (entries outside 0 .. E-1 are skipped; an index that
  *  comes twice in a row counts twice), grad_weights (T, k) fp32; logits, score, renorm and
  *  scale as for moe_route.
- *  grad_logits (T, E) of the logits' type, must not overlap them: written whole.  The choice itself has no gradient; the bias takes none.  Masked experts get 0;
- *  softmax's gradient reaches every expert of the row, unless renorm confines it to the
- *  chosen ones.
+ *  grad_logits (T, E) of the logits' type, must not overlap them: written whole.  The
+ *  choice itself has no gradient; the bias takes none.  Masked experts get 0; softmax's
+ *  gradient reaches every expert of the row, unless renorm confines it to the chosen ones.
  *  Returns as moe_route.
  */
 int moe_route_backward(const void* logits, int type, int64_t T, int64_t E, const int32_t* ids, int32_t k,

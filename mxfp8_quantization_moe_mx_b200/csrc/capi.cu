@@ -233,8 +233,8 @@ int moe_route(const void* logits, int type, int64_t T, int64_t E, const float* b
     if (!route_shape_ok(T, E, k) || E % n_groups != 0) return MXQ_ERR_SHAPE;
     if (T == 0) return MXQ_OK;
     if (!logits || !weights || !ids) return MXQ_ERR_NULL;
-    if (!aligned(logits, type == MXQ_TYPE_BF16 ? 2 : 4) || !aligned(bias, 4) || !aligned(weights, 4) || !aligned(ids, 4))
-        return MXQ_ERR_ALIGN;
+    const uintptr_t size = type == MXQ_TYPE_BF16 ? 2 : 4;
+    if (!aligned(logits, size) || !aligned(bias, 4) || !aligned(weights, 4) || !aligned(ids, 4)) return MXQ_ERR_ALIGN;
     return cuda_status(mxq::launch_moe_route(logits, type == MXQ_TYPE_BF16, T, (int)E, bias, score, n_groups,
                                              top_groups, group_top, k, renorm != 0, scale, weights, ids,
                                              as_stream(stream)));
@@ -313,7 +313,8 @@ int mxfp4_quantize(const void* x_bf16, int64_t batch, int64_t rows, int64_t cols
                    uint8_t* sf_blocked, const int32_t* offs, int32_t G, void* stream) {
     if (batch < 0 || rows < 0 || cols < 0 || G < 0 || cols % 32 != 0 || (G > 0 && batch != 1)) return MXQ_ERR_SHAPE;
     int64_t n = 0;
-    if (!mul_ok(batch, rows, cols, &n) || rows > INT64_MAX / 4 || !mul_ok(batch, rows + 128 * (int64_t)G + 128, cols / 32 + 4, &n))
+    if (!mul_ok(batch, rows, cols, &n) || rows > INT64_MAX / 4 ||
+        !mul_ok(batch, rows + 128 * (int64_t)G + 128, cols / 32 + 4, &n))
         return MXQ_ERR_SHAPE;
     if (batch == 0 || rows == 0 || cols == 0) return MXQ_OK;
     if (!x_bf16 || !q || (!s && !sf_blocked) || (G > 0 && (!offs || !sf_blocked))) return MXQ_ERR_NULL;

@@ -422,7 +422,8 @@ __device__ __forceinline__ bool select_few(const float (&c)[NI], const RouteArgs
         __syncwarp();
         int near = 0;  // candidates that this one may tie with, itself among them
         for (int j = 0; j < cnt; j += 4) {
-            const float4 o = *reinterpret_cast<const float4*>(s->val + j), f = *reinterpret_cast<const float4*>(s->err + j);
+            const float4 o = *reinterpret_cast<const float4*>(s->val + j);
+            const float4 f = *reinterpret_cast<const float4*>(s->err + j);
             rank += before(o.x, v, j < lane) + before(o.y, v, j + 1 < lane) + before(o.z, v, j + 2 < lane) +
                     before(o.w, v, j + 3 < lane);
             // (not of equal infinite ones, which tie by index: their difference is no number)

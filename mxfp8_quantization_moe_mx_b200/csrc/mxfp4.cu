@@ -281,7 +281,8 @@ cudaError_t launch_f4_dequant(const uint8_t* q, const uint8_t* s, uint16_t* y, i
     constexpr int U = 4;
     const int64_t n8 = n / 8;
     const int64_t ctas = (n8 + 256 * U - 1) / (256 * U);
-    return launch_dependent(f4_dequant_kernel<U>, (unsigned)std::min<int64_t>(ctas, 0x7FFFFFFF), 256, 0, stream, q, s, y, n8);
+    return launch_dependent(f4_dequant_kernel<U>, (unsigned)std::min<int64_t>(ctas, 0x7FFFFFFF), 256, 0, stream, q, s,
+                            y, n8);
 }
 
 }  // namespace mxq

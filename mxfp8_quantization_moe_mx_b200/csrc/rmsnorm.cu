@@ -8,11 +8,10 @@
 //
 // Everything is bound by HBM: a row is read once, stays in registers through the two
 // reductions (sum of squares over the CTA, block maxima over four lanes) and leaves as codes.
-// A CTA owns a row at a time; a warp holds 32 V consecutive 8-element vectors of it, lane l the vectors l, l + 32, ..., so
-// four neighbouring lanes hold one 32-element block and a warp's 8 V scale bytes leave in one
-// run.  The sums are fp32: a thread adds
-// at most 32 squares, then 5 shuffle steps and at most 32 warps' sums, so the relative
-// error stays under 2^-18.
+// A warp holds 32 V consecutive 8-element vectors of a row, lane l the vectors l, l + 32, ...,
+// so four neighbouring lanes hold one 32-element block and a warp's 8 V scale bytes leave in
+// one run.  The sums are fp32: a thread adds at most 32 squares, then 5 shuffle steps and at
+// most 32 warps' sums, so the relative error stays under 2^-18.
 
 #include <algorithm>
 #include <type_traits>
@@ -62,7 +61,9 @@ __device__ __forceinline__ f2 mul2(f2 a, f2 b) {
 __device__ __forceinline__ f2 bf2(uint32_t w) { return {bf16_lo(w), bf16_hi(w)}; }
 
 // The i-th pair of a vector of eight bf16.
-__device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) {
+    return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
 
 // Sums of bf16 pairs, rounded once (the exact sum of two bf16 that an fp32 addition would
 // round first is never near a midpoint of bf16, so this is also bf16(fp32 sum)).
@@ -135,8 +136,8 @@ __device__ __forceinline__ uint2 codes8(const uint4& o, uint32_t b) {
 // One row's norm and codes from its packed sums h[] (V vectors per thread), stored.  `base`:
 // the element of the thread's first vector; the others follow 256 elements apart.
 template <int V, typename W>
-__device__ __forceinline__ void norm_row(const uint4 (&h)[V], const W8<W> (&w)[V], float r, int64_t base, int nv, int warp,
-                                         uint16_t* y, uint8_t* __restrict__ q, uint8_t* __restrict__ s) {
+__device__ __forceinline__ void norm_row(const uint4 (&h)[V], const W8<W> (&w)[V], float r, int64_t base, int nv,
+                                         int warp, uint16_t* y, uint8_t* __restrict__ q, uint8_t* __restrict__ s) {
     const int lane = threadIdx.x & 31;
     uint4 o[V];
     uint32_t am[V], top = 0;

@@ -339,7 +339,8 @@ def test_route_many_rows_are_all_written():
 # ---- plan --------------------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("T,k,E", [(0, 4, 8), (1, 1, 1), (1, 8, 128), (7, 3, 5), (256, 8, 16), (255, 8, 300),
-                                   (257, 8, 16), (1000, 6, 1024), (2048, 8, 256), (2049, 8, 256), (3001, 7, 64), (9000, 2, 3), (40000, 3, 1024)])
+                                   (257, 8, 16), (1000, 6, 1024), (1024, 8, 256), (1025, 8, 256), (2049, 8, 256),
+                                   (3001, 7, 64), (9000, 2, 3), (40000, 3, 1024)])
 @pytest.mark.parametrize("kind", ["spread", "one", "none", "foreign"])
 def test_plan(T, k, E, kind):
     g = gen(T + E)
