@@ -228,3 +228,73 @@ def test_experts_held_in_four_bits():
             moe.Mxfp4Experts(bad.to(BF).cuda())
     with pytest.raises(mxq.MxqError):
         experts(x.detach()[:, :128], offs)
+
+
+def test_two_products_at_once():
+    """The few-row and the many-row product on two streams, several times over."""
+    g = gen(12)
+    few = moe.Mxfp4Experts((0.05 * torch.randn(8, 512, 1024, generator=g)).to(BF).cuda())
+    many = moe.Mxfp4Experts((0.05 * torch.randn(2, 2560, 1024, generator=g)).to(BF).cuda())
+    jobs = [(few, torch.randn(16, 1024, generator=g).to(BF).cuda(),
+             torch.arange(2, 18, 2, dtype=torch.int32, device="cuda")),
+            (many, torch.randn(1500, 1024, generator=g).to(BF).cuda(),
+             torch.tensor([700, 1500], dtype=torch.int32, device="cuda"))]
+    want = [e(x, o) for e, x, o in jobs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    for _ in range(4):
+        got = []
+        for (e, x, o), s in zip(jobs, streams):
+            with torch.cuda.stream(s):
+                got.append([e(x, o) for _ in range(3)])
+        torch.cuda.synchronize()
+        for outs, w in zip(got, want):
+            assert all(torch.equal(u, w) for u in outs)
+
+
+@pytest.mark.slow
+def test_offsets_past_32_bits():
+    """Tensors of more than 2^31 elements: their last rows as a call on those rows alone."""
+    D = 16384
+    M = (1 << 31) // D + 300
+    x = torch.empty(M, D, dtype=BF, device="cuda")
+    x[:4].normal_()
+    x[4:-4] = 1.0
+    x[-4:].normal_()
+    w = torch.ones(D, device="cuda")
+    q, s = (torch.empty(M, n, dtype=torch.uint8, device="cuda") for n in (D, D // 32))
+    y, r = torch.empty_like(x), torch.empty(M, device="cuda")
+    mxq.rmsnorm_mx_quantize(x, w, 1e-5, q, s, y=y, rstd=r)
+    for part in (slice(0, 4), slice(M - 4, M)):
+        n = moe.rmsnorm(x[part], w)
+        assert torch.equal(n.y, y[part]) and torch.equal(n.q, q[part]) and torch.equal(n.s, s[part])
+    gx, gw = torch.empty_like(x), torch.empty(D, device="cuda")
+    ws = torch.empty(mxq.rmsnorm_backward_workspace_bytes(M, D), dtype=torch.uint8, device="cuda")
+    mxq.rmsnorm_backward(y, x, w, r, gx, gw, ws)
+    part, gw4 = torch.empty(4, D, dtype=BF, device="cuda"), torch.empty_like(gw)
+    mxq.rmsnorm_backward(y[-4:], x[-4:], w, r[-4:], part, gw4, ws)
+    assert torch.equal(part, gx[-4:])
+    del gx, y, q, s
+    codes, scales = (torch.empty(M, n, dtype=torch.uint8, device="cuda") for n in (D // 2, D // 32))
+    mxq.mxfp4_quantize(x, codes, scales)
+    back = torch.empty_like(x)
+    mxq.mxfp4_dequantize(codes, scales, back)
+    c4, s4, b4 = torch.empty_like(codes[:4]), torch.empty_like(scales[:4]), torch.empty_like(back[:4])
+    mxq.mxfp4_quantize(x[-4:], c4, s4)
+    mxq.mxfp4_dequantize(c4, s4, b4)
+    assert torch.equal(c4, codes[-4:]) and torch.equal(s4, scales[-4:]) and torch.equal(b4, back[-4:])
+    tiles = torch.empty(mxq.mx_scales_blocked_bytes(1, M, D // 32), dtype=torch.uint8, device="cuda")
+    again = torch.empty_like(codes)
+    mxq.mxfp4_quantize(x, again, sf_blocked=tiles)
+    assert torch.equal(again[-4:], c4)
+    want = torch.empty_like(tiles)
+    mxq.mx_scales_to_blocked(scales, want)
+    assert torch.equal(tiles, want)
+    del x, back, codes, again, tiles, want
+    T, E = (1 << 31) // 256 + 77, 256
+    logits = torch.zeros(T, E, dtype=BF, device="cuda")
+    logits[-9:].normal_()
+    wt, ids = moe.route(logits, 4)
+    w9, i9 = moe.route(logits[-9:], 4)
+    assert torch.equal(wt[-9:], w9) and torch.equal(ids[-9:], i9)
+    assert (ids[:-9] == torch.arange(4, dtype=torch.int32, device="cuda")).all()
