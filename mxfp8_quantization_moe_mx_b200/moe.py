@@ -6,10 +6,14 @@ results, and the ones that a model trains through are differentiable.
     p = moe.plan(ids, E)                               # p.offs, p.rows, p.src
     rows = n.y[p.src.long() // k]                      # the experts' rows, sorted
     out = experts(rows, p.offs)                        # moe.Mxfp4Experts, for serving
-    y = (out[p.rows.long()].float() * weights[:, :, None]).sum(1)
+    slots = out[p.rows.clamp(min=0).long()].float().masked_fill(p.rows[:, :, None] < 0, 0.0)
+    y = (slots * weights[:, :, None]).sum(1)
 
 A slot that is routed nowhere (its id is -1) has row -1 and weight 0.  Rows at and past the
-last offset belong to no expert; the products leave them unwritten.
+last offset belong to no expert, and the products leave them unwritten: what lies there may be
+NaN, which a weight of 0 does not remove, so the slots are masked.  Their source is -1 as well
+(the gather above takes the last token for them); where gradients pass through the gather and
+a product that leaves those rows' gradients unwritten, mask `rows` by p.src < 0 alike.
 
 Everything runs in this library's kernels on the tensors' device and its current stream;
 there is no CPU path.
@@ -139,7 +143,8 @@ class Mxfp4Experts:
 
     weights: bf16 (G, N, K), N a multiple of 256 and K of 128; experts(x, offs) is
     x[rows of g] @ weights[g].T for every group g of the end offsets, with x bf16 (M, K)
-    quantized to MXFP4 on the way.  Rows in no group come back unwritten.  No gradient."""
+    quantized to MXFP4 on the way.  Rows in no group come back unwritten (mask them when they
+    are combined, as above).  No gradient."""
 
     def __init__(self, weights: torch.Tensor):
         if not isinstance(weights, torch.Tensor) or weights.dim() != 3:
