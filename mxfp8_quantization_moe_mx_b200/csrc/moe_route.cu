@@ -887,14 +887,16 @@ cudaError_t launch_moe_route(const void* logits, bool bf16, int64_t T, int E, co
     RouteArgs a{bias, T, E, k, n_groups, top_groups, group_top, score, renorm ? 1 : 0, scale, E / n_groups, -1,
                 aligned16(logits)};
     const size_t smem = n_groups > 1 ? (size_t)RT_WARPS * E * sizeof(double) : 0;  // a row per warp, for the groups
+    constexpr int MAX_SMEM = RT_WARPS * 1024 * (int)sizeof(double);                // at the largest E
     return by_width(E, [&](auto ni) {
         constexpr int NI = decltype(ni)::value;
         for (int log = 0; log < 6; ++log)
             if (a.gs == NI << log) a.gl_log = log;
         auto go = [&](auto kernel, auto l) {
-            if (smem > 46 * 1024) {
-                const cudaError_t e =
-                    cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            // Without this opt-in the static memory counts within the 48 KB, too.  It stays with the
+            // kernel, and other host threads launch it: always the same value, never a call's own.
+            if (smem + sizeof(Picked) * RT_WARPS > 47 * 1024) {
+                const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_SMEM);
                 if (e != cudaSuccess) return e;
             }
             return launch_dependent(kernel, route_grid(T), 32 * RT_WARPS, smem, stream, l, a, weights, ids);
