@@ -204,10 +204,13 @@ int64_t plan_workspace_bytes(int64_t n, int E) { return n <= PL_ONE ? 0 : 4 * (i
 
 cudaError_t launch_moe_plan(const int32_t* ids, int64_t n, int E, int32_t* offs, int32_t* rows, int32_t* src,
                             int32_t* ws, cudaStream_t stream) {
-    const size_t smem = (size_t)(2 * PL_WARPS + 2) * E * sizeof(int);  // at most 136 KB
-    if (smem > 48 * 1024) {
+    constexpr int PER_EXPERT = (2 * PL_WARPS + 2) * (int)sizeof(int), MAX_SMEM = 1024 * PER_EXPERT;  // 136 KB
+    const size_t smem = (size_t)E * PER_EXPERT;
+    // Without this opt-in the static memory counts within the 48 KB, too.  It stays with the
+    // kernel, and other host threads launch it: always the same value, never a call's own.
+    if (smem > 47 * 1024) {
         const cudaError_t e =
-            cudaFuncSetAttribute(plan_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            cudaFuncSetAttribute(plan_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_SMEM);
         if (e != cudaSuccess) return e;
     }
     if (n <= PL_ONE) {

@@ -424,17 +424,17 @@ cudaError_t launch_ring(K kernel, int v, int tensors, int64_t M, int D, int64_t 
     const int nv = D / 8, threads = (nv + 32 * v - 1) / (32 * v) * 32;
     const int stage = tensors * D * 2;
     constexpr int TOTAL = 220 * 1024;  // of an SM, with the CTAs' own use (1.5 KB each) left aside
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * stage);
+    constexpr int MAX_SMEM = TOTAL - 2048;
+    static_assert(2 * 3 * 16384 * 2 <= MAX_SMEM, "two stages of the longest rows");
+    // The attribute belongs to the kernel and not to the call, and other host threads launch it
+    // and ask for its occupancy: always the same value, whatever this call takes.
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_SMEM);
     int per_sm = 0;
     if (e == cudaSuccess)
         e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, (size_t)2 * stage);
     if (e != cudaSuccess) return e;
     per_sm = std::max(1, per_sm);
     const int stages = std::max(2, std::min(NORM_MAX_STAGES, (TOTAL / per_sm - 2048) / stage));
-    if (stages > 2) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, stages * stage);
-        if (e != cudaSuccess) return e;
-    }
     *grid = (unsigned)std::min({M, (int64_t)sm_count() * per_sm, max_ctas});
     return launch_dependent(kernel, *grid, threads, (size_t)stages * stage, stream, args..., stages);
 }
