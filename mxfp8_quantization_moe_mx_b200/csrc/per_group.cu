@@ -972,6 +972,22 @@ __global__ void __launch_bounds__(PG_BIG_THREADS, 1) per_group_big_kernel(
 
 namespace {
 
+constexpr int PG_TILE_BIG_BYTES = 80 * 1024;  // the largest bound on a CTA's tile (see the shape orders)
+
+// Opt in to more than 48 KB of shared memory, which without it the static memory counts within,
+// too.  The attribute belongs to the kernel and not to the call, and other host threads launch
+// it: always the same value, that of the largest tile.
+template <typename K>
+cudaError_t allow_tile_smem(K kernel, int smem) {
+    constexpr int STATIC = 2048, MAX_SMEM = PG_TILE_BIG_BYTES + 256;  // pg_tile_smem adds at most 256
+    static_assert(pg_tile_smem(PG_TILE_BIG_BYTES / 128, 64) <= MAX_SMEM &&
+                      pg_tile_smem(PG_TILE_BIG_BYTES / 64, 32) <= MAX_SMEM &&
+                      pg_tile_smem(PG_TILE_BIG_BYTES / 32, 16) <= MAX_SMEM,
+                  "the largest tiles");
+    if (smem + STATIC <= 48 * 1024) return cudaSuccess;
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_SMEM);
+}
+
 template <bool COL_MAJOR, int W, int CL>
 cudaError_t launch_tile(const uint16_t* x, int64_t M, int64_t K, const int32_t* offs, int32_t G, uint8_t* q,
                         float* scales, int r_cap, int rows_per_group, cudaStream_t stream) {
@@ -982,10 +998,8 @@ cudaError_t launch_tile(const uint16_t* x, int64_t M, int64_t K, const int32_t* 
         return cudaErrorInvalidValue;
     const int smem = pg_tile_smem(r_cap, W);
     auto kernel = per_group_tile_kernel<COL_MAJOR, W, CL>;
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
-    }
+    const cudaError_t e = allow_tile_smem(kernel, smem);
+    if (e != cudaSuccess) return e;
     cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((K + W - 1) / W * CL), (unsigned)G);
@@ -1019,11 +1033,8 @@ cudaError_t launch_pair_col(const uint16_t* x, int64_t M, int64_t K, const int32
     if (M > 0 && !encode_bf16_tile_map(&xmap, x, (uint64_t)K, (uint64_t)M, (uint32_t)W, (uint32_t)pg_box_rows(W)))
         return cudaErrorInvalidValue;
     const int smem = pg_tile_smem(r_cap, W);
-    if (smem > 48 * 1024) {
-        const cudaError_t e =
-            cudaFuncSetAttribute(per_group_pair_col_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
-    }
+    const cudaError_t e = allow_tile_smem(per_group_pair_col_kernel, smem);
+    if (e != cudaSuccess) return e;
     cudaFuncSetAttribute(per_group_pair_col_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
                          cudaSharedmemCarveoutMaxShared);
     const dim3 grid((unsigned)((K + W - 1) / W), (unsigned)((G + 1) / 2));
@@ -1076,7 +1087,6 @@ void set_wait_limit_ns(uint64_t ns) { g_wait_limit_ns.store(ns); }
 struct TileShape {
     int w, cl, max_bytes;
 };
-constexpr int PG_TILE_BIG_BYTES = 80 * 1024;
 constexpr TileShape PG_ROW_ORDER[] = {{64, 1, PG_TILE_BIG_BYTES},   {64, 2, PG_TILE_TARGET_BYTES},
                                       {32, 1, PG_TILE_TARGET_BYTES}, {64, 4, PG_TILE_TARGET_BYTES},
                                       {64, 8, PG_TILE_BIG_BYTES},   {32, 2, PG_TILE_TARGET_BYTES},

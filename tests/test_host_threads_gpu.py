@@ -95,6 +95,17 @@ def route(T, E, n_groups, seed):
                            ids.data_ptr(), raw)
     return call, [w, ids]
 
+def per_group(M, K, G, seed):
+    L = mxq.lib()
+    x = torch.randn(M, K, generator=gen(seed)).to(BF).cuda()
+    offs = (torch.arange(1, G + 1, dtype=I32) * (M // G)).cuda()
+    q, s = torch.empty(M, K, dtype=U8, device="cuda"), torch.empty(G, K, device="cuda")
+
+    def call(raw, keep=(x, offs)):
+        return L.fp8_per_group_rowwise_quant(x.data_ptr(), M, K, offs.data_ptr(), G, mxq.ROW_MAJOR, q.data_ptr(),
+                                             s.data_ptr(), raw)
+    return call, [q, s]
+
 
 def test_norm_gradients():
     # 600 rows: more than one per CTA, so that the order of the weight gradient's sums is the grid's
@@ -107,3 +118,11 @@ def test_plans():
 
 def test_grouped_routing():
     at_once([route(16, 1024, 8, 5), route(16, 768, 8, 6)])
+
+
+def test_per_group():
+    sizes = (1150, 64, 2), (800, 64, 2)  # 575 and 400 rows a group: 80 and 58 KB of tile
+    for M, K, G in sizes:
+        plan = mxq.fp8_per_group_rowwise_plan(M, K, G, mxq.ROW_MAJOR)
+        assert (plan["kernel"], plan["slab_cols"], plan["cluster"]) == ("tile", 64, 1), plan
+    at_once([per_group(*size, seed) for seed, size in enumerate(sizes)])

@@ -26,6 +26,27 @@ def routing():
             b = 0.2 * torch.randn(E, generator=gen(E + 1))
             check_route(x, 8, b, score="sigmoid", n_groups=n_groups, top_groups=3, group_top=2, renorm=True)
 
+def per_group():
+    """Average group sizes whose tile, with 288 to 1840 bytes of static memory, passes 48 KB."""
+    import numpy as np
+
+    import mxfp8_quantization_moe_mx_b200 as mxq
+    import oracle
+    from _gpu import bits_of, gpu_per_group, same_f32
+    from mxfp8_quantization_moe_mx_b200 import workloads as wl
+
+    for n, G, layout, width, cluster in ((2400, 3, mxq.ROW_MAJOR, 64, 8), (5460, 2, mxq.ROW_MAJOR, 32, 8),
+                                         (2849, 3, mxq.COL_MAJOR, 16, 2), (5460, 2, mxq.COL_MAJOR, 32, 8),
+                                         (5740, 2, mxq.COL_MAJOR, 16, 4), (11500, 2, mxq.COL_MAJOR, 16, 8)):
+        M, K = n * G, 96
+        plan = mxq.fp8_per_group_rowwise_plan(M, K, G, layout)
+        assert (plan["kernel"], plan["slab_cols"], plan["cluster"]) == ("tile", width, cluster), plan
+        x = wl.stress(seed=n, M=M, K=K, n_groups=3, n_empty=0)["x"]
+        offs = (n * np.arange(1, G + 1)).astype(np.int32)
+        qr, sr = oracle.per_group_quant(bits_of(x), offs, layout)
+        q, s = gpu_per_group(x, offs, layout)
+        assert same_f32(s, sr) and np.array_equal(q, qr), (n, G, layout)
+
 
 def run(family):
     import torch
@@ -41,3 +62,7 @@ def run(family):
 
 def test_grouped_routing_first_in_a_process():
     run("routing")
+
+
+def test_per_group_first_in_a_process():
+    run("per_group")
