@@ -331,8 +331,6 @@ int64_t moe_plan_workspace_bytes(int64_t n, int64_t E);
  *  res_out (M, D) bf16 receives h (NULL: not written); it may be x or residual itself.
  *  y (M, D) bf16 and rstd (M) fp32 (r, for the backward pass) may be NULL.
  *  All (.., D) tensors 16-byte aligned.  Apart from res_out nothing may overlap.
- *  With many rows the kernels here wait, bounded (2 s), for copies into shared memory; a CTA
- *  that gives up leaves its remaining rows unwritten and is counted by mxq_wait_timeouts.
  *  Returns MXQ_OK, MXQ_ERR_ARG (a type, eps), MXQ_ERR_SHAPE, MXQ_ERR_NULL, MXQ_ERR_ALIGN
  *  or MXQ_ERR_CUDA.
  */
@@ -350,6 +348,9 @@ int rmsnorm_mx_quantize(const void* x_bf16, const void* residual_bf16, const voi
  *  grad_res itself.  grad_weight (D) fp32, written whatever M is (zeros for M = 0).
  *  workspace  rmsnorm_backward_workspace_bytes(M, D) bytes, 16-byte aligned, one for each
  *  call that may run at the same time.  The sums' order is fixed for given sizes.
+ *  The kernel waits a bounded time (2 s by default, see mxq_set_wait_limit_ns) for copies
+ *  into shared memory.  A CTA that gives up is counted by mxq_wait_timeouts; its remaining
+ *  rows of grad_x are left unwritten, and grad_weight, which lacks them, is NaN throughout.
  *  Returns as rmsnorm_mx_quantize.
  */
 int rmsnorm_backward(const void* grad_y_bf16, const void* h_bf16, const void* weight, int weight_type,
@@ -417,8 +418,8 @@ const char* mxq_last_cuda_error(void);
  * mxq_wait_timeouts -- diagnostics: *count receives the number of kernel CTAs on the
  * current device, since the library was loaded, that gave up a bounded wait (a copy
  * into shared memory, or a cluster sibling's partial maxima, that did not arrive in
- * time).  Their (group, column-slab) tiles were skipped: codes and scales there were
- * not written.  It is 0 in a healthy run.
+ * time).  What such a CTA leaves unwritten is said at each call: the per-group kernels skip
+ * its (group, column-slab) tile, codes and scales alike.  It is 0 in a healthy run.
  * Synchronous (waits for the device).  Returns MXQ_OK, MXQ_ERR_NULL or MXQ_ERR_CUDA.
  */
 int mxq_wait_timeouts(unsigned int* count);
@@ -434,9 +435,9 @@ int mxq_wait_abandoned(unsigned int* count);
 
 /*
  * mxq_set_wait_limit_ns -- diagnostics: the limit, in nanoseconds, of the bounded waits
- * of every later fp8_per_group_rowwise_quant launch from this process (default
- * MXQ_WAIT_LIMIT_DEFAULT_NS).  0 makes every such wait give up at once, so the give-up
- * path (skipped tiles, counted in mxq_wait_timeouts) can be exercised on purpose; the
+ * of every later fp8_per_group_rowwise_quant and rmsnorm_backward launch from this process
+ * (default MXQ_WAIT_LIMIT_DEFAULT_NS).  0 makes every such wait give up at once, so the
+ * give-up path (counted in mxq_wait_timeouts) can be exercised on purpose; the
  * wait for copies still in flight after giving up keeps its own long limit.  Takes
  * effect at launch; not thread-safe with respect to concurrent launches that expect
  * another limit.  Always returns MXQ_OK.

@@ -249,8 +249,8 @@ def mxq_wait_abandoned() -> int:
 
 
 def mxq_set_wait_limit_ns(ns: int) -> None:
-    """Limit of the per-group kernels' bounded waits for later launches (0: give up at
-    once, to exercise the give-up path)."""
+    """Limit of the bounded waits of the per-group kernels and the norm's gradient for later
+    launches (0: give up at once, to exercise the give-up path)."""
     _check(lib().mxq_set_wait_limit_ns(int(ns)))
 
 

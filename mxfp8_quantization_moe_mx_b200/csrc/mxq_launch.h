@@ -124,7 +124,8 @@ cudaError_t launch_moe_plan(const int32_t* ids, int64_t n, int E, int32_t* offs,
 unsigned int read_wait_timeouts();
 unsigned int read_wait_abandoned();
 
-// Limit of the bounded waits of later per-group launches (0: give up at once).
+// Limit of the bounded waits of later per-group and norm-gradient launches (0: give up at once).
 void set_wait_limit_ns(uint64_t ns);
+uint64_t wait_limit_ns();
 
 }  // namespace mxq

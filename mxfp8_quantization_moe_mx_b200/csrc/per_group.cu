@@ -1069,6 +1069,7 @@ unsigned int read_wait_abandoned() {
 }
 
 void set_wait_limit_ns(uint64_t ns) { g_wait_limit_ns.store(ns); }
+uint64_t wait_limit_ns() { return g_wait_limit_ns.load(); }
 
 // Tile shapes (slab width W, cluster size CL) of the TMA tile kernel, in the order they
 // are tried (each order measured against the alternatives on the per-group shapes).

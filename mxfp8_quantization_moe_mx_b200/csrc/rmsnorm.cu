@@ -257,11 +257,11 @@ __global__ void __launch_bounds__(WARP_ROW ? 256 : 1024) rmsnorm_mx_kernel(
 // works on one, so that the loads in flight do not depend on registers or on how the
 // reductions serialise a row.  Stage s is refilled once the
 // barrier inside the row's reduction has shown that every thread has read it.  A wait that
-// runs out (see mxq_set_wait_limit_ns for how long the library's waits are by default) ends
-// the CTA: it stores nothing more, waits for its copies in flight, and is counted.
+// runs out (see mxq_set_wait_limit_ns) ends the CTA: it stores no more rows, NaN as its share of
+// the weight's gradient, waits for its copies in flight, and is counted.
 __device__ unsigned int g_norm_timeouts = 0;
 
-constexpr uint64_t NORM_WAIT_NS = MXQ_WAIT_LIMIT_DEFAULT_NS, NORM_DRAIN_NS = 20000000000ull;
+constexpr uint64_t NORM_DRAIN_NS = 20000000000ull;
 constexpr int NORM_MAX_STAGES = 4;
 
 struct Ring {
@@ -312,7 +312,7 @@ __device__ __forceinline__ void ring_leave(Ring* ring, int stages, int st, uint3
 template <int V, typename W, bool RES>
 __global__ void __launch_bounds__(512) rmsnorm_backward_kernel(
     const uint16_t* gy, const uint16_t* __restrict__ h, const W* __restrict__ w, const float* __restrict__ rstd,
-    const uint16_t* gres, int64_t M, int D, uint16_t* gx, float* __restrict__ partial, int stages) {
+    const uint16_t* gres, int64_t M, int D, uint16_t* gx, float* __restrict__ partial, uint64_t wait_ns, int stages) {
     constexpr int N = RES ? 3 : 2;
     extern __shared__ __align__(128) uint8_t norm_sm[];
     __shared__ Ring ring;
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(512) rmsnorm_backward_kernel(
     for (int64_t m = blockIdx.x; m < M; m += gridDim.x, turn ^= 1) {
         const int64_t base = m * D + 8 * vec_of<V>(0);
         const float r = __ldg(rstd + m);
-        if (!mbar_wait_bounded(&ring.full[st], phase, NORM_WAIT_NS)) ring.abort = 1;
+        if (!mbar_wait_bounded(&ring.full[st], phase, wait_ns)) ring.abort = 1;
         const uint32_t row = row0 + (uint32_t)(st * N * D * 2);
         uint4 a[V], b[V], e[V];
         f2 dot = {0.0f, 0.0f};
@@ -353,6 +353,9 @@ __global__ void __launch_bounds__(512) rmsnorm_backward_kernel(
         }
         const float mean = cta_sum(dot.x + dot.y, part, turn, true) / (float)D;  // with a barrier: the stage is read
         if (*(volatile int*)&ring.abort) {
+            // the weight's gradient lacks this CTA's rows: NaN in its share shows it
+            const float nan = __int_as_float(0x7FC00000);
+            for (int d = tid; d < D; d += (int)blockDim.x) partial[(int64_t)blockIdx.x * D + d] = nan;
             ring_leave(&ring, stages, st, phase, m, M);
             return;
         }
@@ -463,9 +466,9 @@ cudaError_t norm_backward(const uint16_t* gy, const uint16_t* h, const W* w, con
         auto go = [&](auto vv) {
             constexpr int V = decltype(vv)::value;
             return gres ? launch_ring(rmsnorm_backward_kernel<V, W, true>, V, 3, M, D, NORM_MAX_CTAS, &grid, stream,
-                                      gy, h, w, rstd, gres, M, D, gx, ws)
+                                      gy, h, w, rstd, gres, M, D, gx, ws, wait_limit_ns())
                         : launch_ring(rmsnorm_backward_kernel<V, W, false>, V, 2, M, D, NORM_MAX_CTAS, &grid, stream,
-                                      gy, h, w, rstd, gres, M, D, gx, ws);
+                                      gy, h, w, rstd, gres, M, D, gx, ws, wait_limit_ns());
         };
         const cudaError_t e = v == 1   ? go(std::integral_constant<int, 1>())
                               : v == 2 ? go(std::integral_constant<int, 2>())
