@@ -266,7 +266,9 @@ constexpr int NORM_MAX_STAGES = 4;
 
 struct Ring {
     uint64_t full[NORM_MAX_STAGES];
-    int abort;
+    // whether a thread gave up its wait for the row, for rows in turn: a thread that is past the
+    // row's barrier may give up the next one while others have yet to look at this one's
+    int abort[2];
 };
 
 // N tensors' rows side by side in a stage of N * D bf16.
@@ -283,7 +285,7 @@ template <int N>
 __device__ __forceinline__ void ring_start(uint8_t* sm, Ring* ring, int stages, const uint16_t* const (&from)[3],
                                            int64_t M, int D) {
     if (threadIdx.x == 0) {
-        ring->abort = 0;
+        ring->abort[0] = ring->abort[1] = 0;
         for (int st = 0; st < stages; ++st) mbar_init(&ring->full[st], 1);
         for (int st = 0; st < stages; ++st) {
             const int64_t m = blockIdx.x + (int64_t)st * gridDim.x;
@@ -332,7 +334,7 @@ __global__ void __launch_bounds__(512) rmsnorm_backward_kernel(
     for (int64_t m = blockIdx.x; m < M; m += gridDim.x, turn ^= 1) {
         const int64_t base = m * D + 8 * vec_of<V>(0);
         const float r = __ldg(rstd + m);
-        if (!mbar_wait_bounded(&ring.full[st], phase, wait_ns)) ring.abort = 1;
+        if (!mbar_wait_bounded(&ring.full[st], phase, wait_ns)) *(volatile int*)&ring.abort[turn] = 1;
         const uint32_t row = row0 + (uint32_t)(st * N * D * 2);
         uint4 a[V], b[V], e[V];
         f2 dot = {0.0f, 0.0f};
@@ -352,7 +354,7 @@ __global__ void __launch_bounds__(512) rmsnorm_backward_kernel(
             }
         }
         const float mean = cta_sum(dot.x + dot.y, part, turn, true) / (float)D;  // with a barrier: the stage is read
-        if (*(volatile int*)&ring.abort) {
+        if (*(volatile int*)&ring.abort[turn]) {
             // the weight's gradient lacks this CTA's rows: NaN in its share shows it
             const float nan = __int_as_float(0x7FC00000);
             for (int d = tid; d < D; d += (int)blockDim.x) partial[(int64_t)blockIdx.x * D + d] = nan;

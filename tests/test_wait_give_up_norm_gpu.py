@@ -57,3 +57,22 @@ def test_every_wait_gives_up(M, D, with_res):
     assert torch.isnan(lost).all()
     again, gw2, n = run(mxq.WAIT_LIMIT_DEFAULT_NS)
     assert n == 0 and torch.equal(again, gx) and torch.equal(gw2, gw)
+
+
+@pytest.mark.parametrize("limit", [1, 300, 1000])
+@pytest.mark.parametrize("M,D", [(3000, 512), (2000, 5120)])
+def test_some_waits_give_up(M, D, limit):
+    """Limits near a copy's own time: some CTAs give up, some of them after several rows.  A row
+    is written whole and right or not at all."""
+    run = operands(M, D, True)
+    gx, gw, _ = run(mxq.WAIT_LIMIT_DEFAULT_NS)
+    for _ in range(5):
+        bits, got, n = run(limit)
+        untouched = (bits.view(torch.uint8) == CANARY).all(1)
+        assert ((bits == gx).all(1) | untouched).all()
+        if n:
+            assert untouched.any() and torch.isnan(got).all()
+        else:
+            assert torch.equal(bits, gx) and torch.equal(got, gw)
+    again, gw2, n = run(mxq.WAIT_LIMIT_DEFAULT_NS)
+    assert n == 0 and torch.equal(again, gx) and torch.equal(gw2, gw)
