@@ -295,6 +295,8 @@ int moe_route(const void* logits, int type, int64_t T, int64_t E, const float* b
  *  grad_logits (T, E) of the logits' type, must not overlap them: written whole.  The
  *  choice itself has no gradient; the bias takes none.  Masked experts get 0; softmax's
  *  gradient reaches every expert of the row, unless renorm confines it to the chosen ones.
+ *  Renormalised sigmoid: the 1e-20's own part of a gradient, weight (1 - p) times
+ *  1e-20 / (sum p + 1e-20), is 0 where that quotient is at most 2^-53 (so with k = 1 the whole).
  *  Returns as moe_route.
  */
 int moe_route_backward(const void* logits, int type, int64_t T, int64_t E, const int32_t* ids, int32_t k,
@@ -427,7 +429,8 @@ int mxq_wait_timeouts(unsigned int* count);
 /*
  * mxq_wait_abandoned -- diagnostics: of the CTAs counted by mxq_wait_timeouts, those
  * whose copies in flight into their shared memory had still not landed 20 s after they
- * gave up.  Such a CTA exited anyway, so a late copy may have written into shared memory
+ * gave up.  (The per-group kernels' alone: the norm's gradient and the products wait as long
+ * before they leave, and do not count it apart.)  Such a CTA exited anyway, so a late copy may have written into shared memory
  * that a later CTA owns: every output of every launch since is then undefined.  0 in a
  * healthy run.  Synchronous.  Returns MXQ_OK, MXQ_ERR_NULL or MXQ_ERR_CUDA.
  */

@@ -16,7 +16,8 @@
 // instead, __match_any_sync, cost 30 us for 22: its time grows with the distinct values).
 //
 // The bytes (12 per slot) are few: what it costs is the launches and the latency of each
-// step.
+// step, and for many slots the counts, which every CTA of place reads whole before it can place
+// any (524288 slots, 256 experts: 150 KB a CTA, 22 MB of the 26 that come from L2; 15 us).
 
 #include <algorithm>
 

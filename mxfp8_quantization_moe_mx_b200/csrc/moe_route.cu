@@ -471,7 +471,11 @@ __device__ __noinline__ int choose_exact(const L* row, RouteArgs a, double* sc, 
 }
 
 // MODE: what is known when the kernel is compiled, which frees registers and a quarter of the
-// instructions (65536 x 256 in 8 groups: 59 us against 77).
+// instructions (65536 x 256 in 8 groups: 59 us against 77).  Everything else takes ROUTE_ANY:
+// softmax with a bias, groups without one, groups that are not runs of whole lanes, and rows of
+// more than 256, for which the modes have not been tried (65536 rows, fp32, with sigmoid and
+// bias / in 8 groups too / softmax without a bias: 384 experts 133 / 291 / 79 us, 512 experts
+// 149 / 172 / 79, 1024 experts 474 / 524 / 189; 256 by their modes 45 / 57 / 31).
 enum { ROUTE_ANY = 0, ROUTE_SIGMOID_BIAS_GROUPS = 1, ROUTE_SIGMOID_BIAS = 2, ROUTE_PLAIN = 3 };
 template <int NI, typename L, int MODE>
 __global__ void __launch_bounds__(32 * RT_WARPS, NI <= 8 ? 4 : NI <= 16 ? 2 : 1)
@@ -826,7 +830,9 @@ __global__ void __launch_bounds__(32 * RT_WARPS) moe_route_backward_kernel(
                 if (!mine) p = 0.0f;
                 if (a.renorm) {
                     const float inv = 1.0f / (warp_sum(p) + 1e-20f), r = p * inv;
-                    // the constant's own part, down to what 64 bits hold next to 1
+                    // The constant's own part of the formula, g r q 1e-20 / S; where it is under
+                    // 2^-53 of g r q it is taken as 0.  That is far below fp32's rounding of a
+                    // sum over pairs; where that sum is empty (k = 1) the gradient is then 0.
                     const float rest = 1e-20f * inv > 0x1p-53f ? 1e-20f * inv : 0.0f;
                     d = r * q * fmaf(g, rest, pair_sum(r, g, a.k, lane, pairs));
                 } else {
@@ -906,7 +912,7 @@ cudaError_t launch_moe_route(const void* logits, bool bf16, int64_t T, int E, co
             return bf16 ? go(moe_route_kernel<NI, uint16_t, MODE>, static_cast<const uint16_t*>(logits))
                         : go(moe_route_kernel<NI, float, MODE>, static_cast<const float*>(logits));
         };
-        if constexpr (NI <= 8) {  // rows of more than 256: the general form alone
+        if constexpr (NI <= 8) {
             if (bias && score == 1 && n_groups > 1 && a.gl_log >= 0)
                 return typed(std::integral_constant<int, ROUTE_SIGMOID_BIAS_GROUPS>());
             if (bias && score == 1 && n_groups == 1) return typed(std::integral_constant<int, ROUTE_SIGMOID_BIAS>());

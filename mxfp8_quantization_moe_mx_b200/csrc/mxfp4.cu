@@ -101,9 +101,10 @@ __global__ void __launch_bounds__(256) f4_quant_kernel(const uint16_t* __restric
 // ---- with scales in the tensor cores' tiles: a CTA per padded 128-row tile x 512 columns
 // (16 scale columns, 4 scale tiles).  Warp w takes rows w, w + 8, ... of the tile, 1024
 // bytes of a row per step; scales gather in shared memory and leave as whole 16-byte lines.
-// 16411 x 5120 over 16 groups: 45 us, 4.7 TB/s.  What it lacks to a copy is each CTA's search
-// for its group, before its first load: CTAs of a quarter of this took 59 us, four rows a step
-// (fewer CTAs at a time) 54, one row 50.
+// 16411 x 5120 over 16 groups: 45 us, 4.7 TB/s (plain scales 33).  What it lacks to a copy is each
+// CTA's search for its group, before its first load: CTAs of a quarter of this took 59 us, four
+// rows a step (fewer CTAs at a time) 54, one row 50.  Five CTAs per SM leave 48 registers, of
+// which 32 bytes a thread are spilled.
 __global__ void __launch_bounds__(256, 5) f4_quant_blocked_kernel(const uint16_t* __restrict__ x, int64_t rows,
                                                                int64_t cols, uint8_t* __restrict__ q,
                                                                uint8_t* __restrict__ s, uint8_t* __restrict__ sf,

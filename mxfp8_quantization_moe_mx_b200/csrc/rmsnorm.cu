@@ -204,6 +204,9 @@ __device__ __forceinline__ float sum_squares(const uint4 (&h)[V]) {
 //              one 441; persistent CTAs with a ring of bulk-copied rows 395
 //   D = 16384  four 1108, two 1471;  D = 2560  173, 180;  D = 1536  106, 107
 //   D = 1024   two 72, a warp per row 79;  D = 512  a warp 39, two 69;  D = 256  21, 68
+// fp32 weights take the same forms, though only D = 5120 was measured with them: four vectors
+// 404 us.  They need more registers than the 64 that the bound of 1024 threads leaves (88 bytes
+// a thread are spilled).  With y and rstd written too: bf16 443, fp32 481.
 template <int V, bool WARP_ROW, typename W>
 __global__ void __launch_bounds__(WARP_ROW ? 256 : 1024) rmsnorm_mx_kernel(
     const uint16_t* x, const uint16_t* residual, const W* __restrict__ w, int64_t M, int D, float eps,
@@ -247,18 +250,15 @@ __global__ void __launch_bounds__(WARP_ROW ? 256 : 1024) rmsnorm_mx_kernel(
 // ---- gradient ------------------------------------------------------------------------------------
 //
 // With n = h r and g = gy w:  gx = r (g - n mean_d(g n)) + gres,  gw = sum_m gy n.
-// A CTA walks rows blockIdx.x, + gridDim.x, ... and keeps its share of gw in registers
-// (fp32), writes it to its row of the workspace, and a second kernel adds the CTAs' rows in
-// order: no atomics, the same bits every time.
-// ---- a ring of rows in shared memory --------------------------------------------------------------
+// The CTAs persist: each walks rows blockIdx.x, + gridDim.x, ..., keeps its share of gw in
+// registers (fp32) and writes it to its row of the workspace; a second kernel adds the CTAs'
+// rows in order: no atomics, the same bits every time.
 //
-// The gradient's CTAs persist, to keep their share of the weight's gradient.  A CTA walks rows
-// blockIdx.x, + gridDim.x, ... and bulk copies bring its next rows into shared memory while it
-// works on one, so that the loads in flight do not depend on registers or on how the
-// reductions serialise a row.  Stage s is refilled once the
-// barrier inside the row's reduction has shown that every thread has read it.  A wait that
-// runs out (see mxq_set_wait_limit_ns) ends the CTA: it stores no more rows, NaN as its share of
-// the weight's gradient, waits for its copies in flight, and is counted.
+// Bulk copies bring a CTA's next rows into a ring in shared memory while it works on one, so that
+// the loads in flight do not depend on registers or on how the reductions serialise a row.  Stage
+// s is refilled once the barrier inside the row's reduction has shown that every thread has read
+// it.  A wait that runs out (see mxq_set_wait_limit_ns) ends the CTA: it stores no more rows, NaN
+// as its share of gw, waits for its copies in flight, and is counted.
 __device__ unsigned int g_norm_timeouts = 0;
 
 constexpr uint64_t NORM_DRAIN_NS = 20000000000ull;
