@@ -16,10 +16,19 @@ namespace {
 
 thread_local char g_last_cuda_error[256] = "";
 
+// The runtime keeps a refused call's error for this thread until it is read, and the launches
+// that end in cudaGetLastError() would report it for a later, correct call: read it here.
 int cuda_status(cudaError_t e) {
     if (e == cudaSuccess) return MXQ_OK;
+    (void)cudaGetLastError();
     std::strncpy(g_last_cuda_error, cudaGetErrorString(e), sizeof(g_last_cuda_error) - 1);
     g_last_cuda_error[sizeof(g_last_cuda_error) - 1] = '\0';
+    return MXQ_ERR_CUDA;
+}
+
+// The status of a diagnostic read that failed.
+int failed_read() {
+    cuda_status(cudaPeekAtLastError());
     return MXQ_ERR_CUDA;
 }
 
@@ -377,7 +386,8 @@ int mxq_wait_timeouts(unsigned int* count) {
     if (!count) return MXQ_ERR_NULL;
     const unsigned int n = mxq::read_wait_timeouts(), m = mxq::read_gemm_timeouts(),
                        f = mxq::read_f4_gemm_timeouts(), r = mxq::read_norm_timeouts();
-    if (n == 0xFFFFFFFFu || m == 0xFFFFFFFFu || f == 0xFFFFFFFFu || r == 0xFFFFFFFFu) return MXQ_ERR_CUDA;
+    if (n == 0xFFFFFFFFu || m == 0xFFFFFFFFu || f == 0xFFFFFFFFu || r == 0xFFFFFFFFu)
+        return failed_read();
     *count = n + m + f + r;
     return MXQ_OK;
 }
@@ -385,7 +395,7 @@ int mxq_wait_timeouts(unsigned int* count) {
 int mxq_wait_abandoned(unsigned int* count) {
     if (!count) return MXQ_ERR_NULL;
     const unsigned int n = mxq::read_wait_abandoned();
-    if (n == 0xFFFFFFFFu) return MXQ_ERR_CUDA;
+    if (n == 0xFFFFFFFFu) return failed_read();
     *count = n;
     return MXQ_OK;
 }
